@@ -1,0 +1,237 @@
+// Routes sorted by expert, from the caller's expert ids: the stable order that
+// groups routes r = t*K + k by expert, with the routes of experts outside
+// [0, E) left out (experts of other GPUs, dropped tokens).
+//
+// A counting sort. A block of 16 waves owns `chunk` consecutive routes, each
+// wave a contiguous 16th of them. Inside a wave the 64 routes of one step find
+// their peers (routes of the same expert) by one ballot per bit of the key, so
+// the rank among the peers is a population count and no atomic decides a
+// position. Positions follow as base of the expert (routes of lower experts,
+// and of this expert in earlier blocks) + routes of the expert in earlier waves
+// + in earlier steps of the wave + the rank. Left-out routes form a last group
+// with key E, which gives every entry of both maps a writer.
+#include "moe_args.h"
+#include "moe_route_dev.h"
+
+namespace moe {
+
+constexpr int kSortWaves = 16;
+constexpr int kSortMinChunk = kSortWaves * 64;
+constexpr int kSortMaxChunk = 32768;         // per-wave counters are 16-bit
+constexpr long long kSortMaxR = 1LL << 26;
+constexpr long long kSortOneBlock = 4096;    // routes sorted by a single block
+
+__host__ __device__ inline int sort_row_words(int E) { return (E + 2) / 2; }  // E + 1 16-bit counts
+
+template <typename ID>
+__device__ __forceinline__ int sort_key(const ID* __restrict__ ids, long long r, int R, int E) {
+    if (r >= R) return -1;
+    const ID v = ids[r];
+    return v >= 0 && v < (ID)E ? (int)v : E;
+}
+
+// Lanes with the same key as this one (lanes without a route, key -1, aside).
+__device__ __forceinline__ uint64_t peers_of(int key, int nbits) {
+    uint64_t peers = __ballot(key >= 0);
+    for (int b = 0; b < nbits; ++b) {
+        const bool bit = (key >> b) & 1;
+        const uint64_t bal = __ballot(key >= 0 && bit);
+        peers &= bit ? bal : ~bal;
+    }
+    return peers;
+}
+
+// Routes of each expert in one chunk, as 16-bit counts, two per word.
+template <typename ID>
+__global__ __launch_bounds__(1024) void sort_count_kernel(const ID* __restrict__ ids, int R, int E,
+                                                          int chunk, uint32_t* __restrict__ counts) {
+    __shared__ int32_t h[kMaxE + 2];
+    const int words = sort_row_words(E);
+    for (int e = threadIdx.x; e < 2 * words; e += 1024) h[e] = 0;
+    __syncthreads();
+    const long long base = (long long)blockIdx.x * chunk;
+    for (int i = threadIdx.x; i < chunk; i += 1024) {
+        const int key = sort_key(ids, base + i, R, E);
+        if (key >= 0) atomicAdd(&h[key], 1);
+    }
+    __syncthreads();
+    for (int w = threadIdx.x; w < words; w += 1024)
+        counts[(size_t)blockIdx.x * words + w] = (uint32_t)h[2 * w] | ((uint32_t)h[2 * w + 1] << 16);
+}
+
+// The positions of one chunk's routes. counts: the chunks' counts (null when
+// one block sorts everything). Every block sums the counts of all chunks and of
+// those before its own by itself: that reads nblk * (E + 1) 16-bit values from
+// the L2 and saves a launch for a scan.
+template <typename ID>
+__global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__ ids, int R, int E,
+                                                          int chunk, const uint32_t* __restrict__ counts,
+                                                          int32_t* __restrict__ row_to_route,
+                                                          int32_t* __restrict__ route_to_row,
+                                                          int32_t* __restrict__ offsets) {
+    __shared__ uint16_t wcount[kSortWaves][kMaxE + 2];
+    __shared__ int32_t total[kMaxE + 2], before[kMaxE + 2];
+    __shared__ int32_t base[kMaxE + 1];
+    __shared__ int32_t wsum[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int words = sort_row_words(E), nblk = gridDim.x, blk = blockIdx.x;
+    int nbits = 0;
+    while ((1 << nbits) <= E) ++nbits;
+    for (int i = tid; i < kSortWaves * 2 * words; i += 1024) wcount[i / (2 * words)][i % (2 * words)] = 0;
+    for (int e = tid; e < 2 * words; e += 1024) total[e] = before[e] = 0;
+    __syncthreads();
+
+    // routes per expert of this wave
+    const int per = chunk / kSortWaves;
+    const long long r0 = (long long)blk * chunk + (long long)wave * per;
+    for (int s = 0; s < per; s += 64) {
+        const int key = sort_key(ids, r0 + s + lane, R, E);
+        const uint64_t peers = peers_of(key, nbits);
+        if (key >= 0 && (peers & ((1ull << lane) - 1ull)) == 0)
+            wcount[wave][key] = (uint16_t)(wcount[wave][key] + __popcll(peers));
+        asm volatile("" ::: "memory");  // the next step reads what other lanes wrote (LDS keeps a wave's order)
+    }
+    // routes per expert of all chunks and of the chunks before this one
+    if (counts) {
+        // the chunks are dealt to groups of `words` threads, one word (two experts) per thread
+        const int groups = 1024 / words, w = tid % words, q = tid / words;
+        if (q < groups) {
+            int a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+            for (int b = q; b < nblk; b += groups) {
+                const uint32_t v = counts[(size_t)b * words + w];
+                const int lo = (int)(v & 0xFFFF), hi = (int)(v >> 16);
+                a0 += lo;
+                a1 += hi;
+                b0 += b < blk ? lo : 0;
+                b1 += b < blk ? hi : 0;
+            }
+            atomicAdd(&total[2 * w], a0);
+            atomicAdd(&total[2 * w + 1], a1);
+            atomicAdd(&before[2 * w], b0);
+            atomicAdd(&before[2 * w + 1], b1);
+        }
+    }
+    __syncthreads();
+    // exclusive prefix over the waves; the chunk's counts are the totals when it is the only one
+    for (int e = tid; e <= E; e += 1024) {
+        int run = 0;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int v = wcount[w][e];
+            wcount[w][e] = (uint16_t)run;
+            run += v;
+        }
+        if (!counts) total[e] = run;
+    }
+    __syncthreads();
+    // exclusive prefix over the experts (E <= 1024, one thread each)
+    const int mine = tid < E ? total[tid] : 0;
+    const int incl = wave_incl_scan(mine);
+    if (lane == 63) wsum[wave] = incl;
+    __syncthreads();
+    int lower = 0, kept = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) lower += wsum[w];
+        kept += wsum[w];
+    }
+    const int off = lower + incl - mine;
+    if (tid < E) {
+        base[tid] = off + before[tid];
+        if (blk == 0) offsets[tid] = off;
+    }
+    if (tid == 0) {
+        base[E] = kept + before[E];
+        if (blk == 0) offsets[E] = kept;
+    }
+    __syncthreads();
+    for (int s = 0; s < per; s += 64) {
+        const long long r = r0 + s + lane;
+        const int key = sort_key(ids, r, R, E);
+        const uint64_t peers = peers_of(key, nbits);
+        const int rank = __popcll(peers & ((1ull << lane) - 1ull));
+        int prior = 0;
+        if (key >= 0) prior = wcount[wave][key];
+        asm volatile("" ::: "memory");
+        if (key >= 0 && rank == 0) wcount[wave][key] = (uint16_t)(prior + __popcll(peers));
+        asm volatile("" ::: "memory");
+        if (key >= 0) {
+            const int row = base[key] + prior + rank;
+            row_to_route[row] = key < E ? (int)r : -1;
+            route_to_row[r] = key < E ? row : -1;
+        }
+    }
+}
+
+// Routes per block: the smallest power of two from kSortMinChunk that keeps the
+// blocks at 256 or fewer (each reads every block's counts), up to the largest.
+static int sort_chunk(long long R) {
+    int c = kSortMinChunk;
+    while (c < kSortMaxChunk && (R + c - 1) / c > 256) c *= 2;
+    return c;
+}
+
+template <typename ID>
+static hipError_t launch_sort(const ID* ids, int R, int E, uint32_t* counts, int32_t* row_to_route,
+                              int32_t* route_to_row, int32_t* offsets, hipStream_t s) {
+    if (R <= kSortOneBlock) {
+        const int chunk = (R + kSortMinChunk - 1) / kSortMinChunk * kSortMinChunk;
+        hipLaunchKernelGGL(sort_place_kernel<ID>, dim3(1), dim3(1024), 0, s, ids, R, E, chunk,
+                           (const uint32_t*)nullptr, row_to_route, route_to_row, offsets);
+    } else {
+        const int chunk = sort_chunk(R);
+        const int nblk = (R + chunk - 1) / chunk;
+        hipLaunchKernelGGL(sort_count_kernel<ID>, dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk, counts);
+        hipLaunchKernelGGL(sort_place_kernel<ID>, dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk,
+                           (const uint32_t*)counts, row_to_route, route_to_row, offsets);
+    }
+    return hipGetLastError();
+}
+
+static int check_sort_sizes(int32_t T, int32_t K, int32_t E) {
+    if (E < 1 || E > kMaxE) return reject(MOE_ERR_INVALID, "E=%d outside [1, %d]", E, kMaxE);
+    if (T < 0) return reject(MOE_ERR_INVALID, "T=%d is negative", T);
+    if (K < 1 || K > kMaxK) return reject(MOE_ERR_INVALID, "K=%d outside [1, %d]", K, kMaxK);
+    if ((long long)T * K > kSortMaxR)
+        return reject(MOE_ERR_UNSUPPORTED, "T*K=%lld routes above %lld", (long long)T * K, kSortMaxR);
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t E) {
+    if (check_sort_sizes(T, K, E) != MOE_OK) return 0;
+    const long long R = (long long)T * K;
+    if (R <= kSortOneBlock) return 256;
+    const int chunk = sort_chunk(R);
+    return align256((size_t)((R + chunk - 1) / chunk) * sort_row_words(E) * 4);
+}
+
+extern "C" int moe_sort_routes(const void* ids, int32_t ids_are_wide, int32_t T, int32_t K, int32_t E,
+                               void* workspace, size_t workspace_bytes, int32_t* row_to_route,
+                               int32_t* route_to_row, int32_t* offsets, hipStream_t stream) {
+    const int rc = check_sort_sizes(T, K, E);
+    if (rc) return rc;
+    if (ids_are_wide != 0 && ids_are_wide != 1) return reject(MOE_ERR_INVALID, "ids_are_wide must be 0 or 1");
+    const size_t R = (size_t)T * K;
+    if (!offsets || !workspace || (R && (!ids || !row_to_route || !route_to_row)))
+        return reject(MOE_ERR_INVALID, "NULL pointer argument");
+    if (!is_aligned(ids, ids_are_wide ? 8 : 4) || !is_aligned(row_to_route, 4) || !is_aligned(route_to_row, 4) ||
+        !is_aligned(offsets, 4) || !is_aligned(workspace, 16))
+        return reject(MOE_ERR_INVALID, "misaligned pointer");
+    const size_t need = moe_sort_workspace_bytes(T, K, E);
+    if (workspace_bytes < need)
+        return reject(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    const struct { const void* p; size_t n; } b[] = {{ids, R * (ids_are_wide ? 8 : 4)}, {workspace, need},
+                                                    {row_to_route, R * 4}, {route_to_row, R * 4},
+                                                    {offsets, ((size_t)E + 1) * 4}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(b[i].p, b[i].n, b[j].p, b[j].n)) return reject(MOE_ERR_INVALID, "buffers overlap");
+    uint32_t* counts = static_cast<uint32_t*>(workspace);
+    return launched(ids_are_wide ? launch_sort(static_cast<const int64_t*>(ids), (int)R, E, counts, row_to_route,
+                                               route_to_row, offsets, stream)
+                                 : launch_sort(static_cast<const int32_t*>(ids), (int)R, E, counts, row_to_route,
+                                               route_to_row, offsets, stream),
+                    "sort routes");
+}

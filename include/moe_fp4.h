@@ -220,6 +220,105 @@ int moe_workspace_view(const moe_dims* d, int32_t T, int32_t K, int32_t mode, in
 int moe_stage_timing(int32_t enable);
 int moe_stage_times(float* ms, int32_t n, int32_t* forwards);
 
+/* -------------------------------------------------------------------------
+ * Operators around the experts, each as a call of its own
+ * -------------------------------------------------------------------------
+ * The routes of T tokens with K experts each (route r = t*K + k) sorted by
+ * expert, token rows dispatched to the experts' rows and combined back with
+ * the router's weights, the gradients of both, and products of 8-bit integer
+ * matrices with a scale for each token and each output channel.
+ *
+ * Row strides are in elements; the elements of a row are contiguous. Pointers
+ * are aligned to their element unless noted. Outputs must not share bytes with
+ * inputs or with each other (MOE_ERR_INVALID). T = 0 (or no rows) is valid and
+ * only writes what does not depend on rows. Nothing is kept between calls, so
+ * calls on different streams are independent as long as their buffers are. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 } moe_dtype;
+
+/* Workspace bytes of moe_sort_routes (0 if the sizes are invalid). */
+size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t E);
+
+/* Stable sort of the routes by expert.
+ *   ids: [T][K] expert ids, int32 (ids_are_wide = 0) or int64 (1). An id
+ *   outside [0, E) drops its route (an expert of another GPU, a token that is
+ *   not to be routed); the same expert may appear twice in a token.
+ *   row_to_route: [T*K] route of each row; routes of expert e fill the rows
+ *   offsets[e] .. offsets[e+1]-1 in ascending order; -1 in the rows from
+ *   offsets[E] on.   route_to_row: [T*K] the row of each route, -1 if dropped.
+ *   offsets: [E+1].   workspace: >= moe_sort_workspace_bytes(T, K, E) bytes,
+ *   16-byte aligned.   1 <= E <= 1024, 1 <= K <= 64, T*K <= 2^26. */
+int moe_sort_routes(const void* ids, int32_t ids_are_wide, int32_t T, int32_t K, int32_t E,
+                    void* workspace, size_t workspace_bytes, int32_t* row_to_route,
+                    int32_t* route_to_row, int32_t* offsets, hipStream_t stream);
+
+/* rows[route_to_row[t*K+k]] = w[t,k] * x[t] for every route that is kept.
+ *   x: [T][H], rows: [T*K][H], both of type `dtype` (moe_dtype). weights:
+ *   [T][K] fp32, or NULL for 1 (the rows are then copies, bit for bit). Rows
+ *   that no route names are left as they were. An entry of route_to_row outside
+ *   [0, T*K) counts as dropped. 1 <= H <= 2^20, T*K <= 2^26. x_stride may be
+ *   anything from 0 (one row for all tokens) on. */
+int moe_dispatch(const void* x, int64_t x_stride, int32_t dtype, const int32_t* route_to_row,
+                 const float* weights, int32_t T, int32_t K, int32_t H, void* rows,
+                 int64_t rows_stride, hipStream_t stream);
+
+/* Gradients of moe_dispatch from the gradient of its rows:
+ *   dx[t] = sum_k w[t,k] drows[row(t,k)]   (fp32 sums, k ascending, one rounding)
+ *   dweights[t,k] = <x[t], drows[row(t,k)]>   (fp32; 0 for a dropped route)
+ *   dweights may be NULL (x is then not read, and may be NULL); it needs weights. */
+int moe_dispatch_grad(const void* drows, int64_t drows_stride, int32_t dtype,
+                      const int32_t* route_to_row, const float* weights, const void* x,
+                      int64_t x_stride, int32_t T, int32_t K, int32_t H, void* dx,
+                      int64_t dx_stride, float* dweights, hipStream_t stream);
+
+/* y[t] = sum_k w[t,k] rows[route_to_row[t*K+k]]: fp32 sums, k ascending, one
+ * rounding to `dtype`; dropped routes are skipped (their rows, whatever they
+ * hold, are not read), a token without routes gets zeros. Like moe_finalize, for
+ * sorted routes with drops, every moe_dtype and strided rows. */
+int moe_combine(const void* rows, int64_t rows_stride, int32_t dtype, const int32_t* route_to_row,
+                const float* weights, int32_t T, int32_t K, int32_t H, void* y, int64_t y_stride,
+                hipStream_t stream);
+
+/* Gradients of moe_combine from dy: [T][H]:
+ *   drows[row(t,k)] = w[t,k] dy[t]; rows that no route names are left as they were
+ *   dweights[t,k] = <dy[t], rows[row(t,k)]>; may be NULL (rows is then not read). */
+int moe_combine_grad(const void* dy, int64_t dy_stride, int32_t dtype, const int32_t* route_to_row,
+                     const float* weights, const void* rows, int64_t rows_stride, int32_t T,
+                     int32_t K, int32_t H, void* drows, int64_t drows_stride, float* dweights,
+                     hipStream_t stream);
+
+/* Symmetric 8-bit quantization of each row: scales[m] = max_j |x[m,j]| / 127 in
+ * fp32, codes[m,j] = x[m,j] / scales[m] rounded to the nearest integer, ties to
+ * even (the exact quotient of the fp32 scale, so the codes are reproducible bit
+ * for bit), in [-127, 127]. A zero row has scale 0 and codes 0; a row with an
+ * infinity or a NaN has that as its scale and codes 0 (products with it are NaN).
+ *   x: [rows][cols] of type dtype, codes: [rows][cols].  1 <= cols <= 2^20. */
+int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, int32_t rows, int32_t cols,
+                     int8_t* codes, int64_t codes_stride, float* scales, hipStream_t stream);
+
+/* y[m,n] = a_scales[m] b_scales[n] sum_k a[m,k] b[n,k] + bias[n]: exact 32-bit
+ * integer sums, scales and bias in fp32, one rounding to out_dtype (moe_dtype).
+ *   a: [M][K], b: [N][K] int8, 16-byte aligned with strides that are multiples
+ *   of 16; bias: [N] fp32 or NULL; y: [M][N].  K a multiple of 16 below 131072
+ *   (MOE_ERR_UNSUPPORTED otherwise), N <= 2^20, M <= 2^26. */
+int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, const int8_t* b,
+                   int64_t b_stride, const float* b_scales, const float* bias, int32_t M, int32_t N,
+                   int32_t K, int32_t out_dtype, void* y, int64_t y_stride, hipStream_t stream);
+
+/* The same product expert by expert on sorted rows: the rows offsets[e] ..
+ * offsets[e+1]-1 of y use b[e] ([E][N][K], experts b_expert_stride bytes
+ * apart), b_scales[e] ([E][N]) and bias[e] ([E][N] or NULL). Rows of y outside
+ * the offsets are left as they were.
+ *   row_to_route NULL: row r of y uses row r of a (a_rows = M).
+ *   Otherwise row r uses row row_to_route[r] / topk of a, the token's (a_rows =
+ *   M / topk tokens): FC1 needs no dispatched copy. Rows whose entry names no
+ *   token are left as they were. */
+int moe_int_grouped_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, int32_t a_rows,
+                           const int8_t* b, int64_t b_stride, int64_t b_expert_stride,
+                           const float* b_scales, const float* bias, const int32_t* offsets,
+                           const int32_t* row_to_route, int32_t topk, int32_t M, int32_t N,
+                           int32_t K, int32_t E, int32_t out_dtype, void* y, int64_t y_stride,
+                           hipStream_t stream);
+
 /* Message for the last non-OK status returned on this thread. */
 const char* moe_last_error(void);
 
