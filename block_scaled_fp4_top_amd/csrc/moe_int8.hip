@@ -5,12 +5,18 @@
 //   product:  y[m,n] = sa[m] sb[n] sum_k a[m,k] b[n,k] (+ bias[n])
 // The sums are exact 32-bit integers (|sum| <= 2^14 * 131056 < 2^31), the scales
 // are applied in fp32 and the result is rounded once to the output's type.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
 #include "moe_args.h"
 #include "moe_rows_dev.h"
+#include "moe_route_dev.h"
 
 namespace moe {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // quantizer
@@ -81,10 +87,32 @@ struct Int8Args {
     int64_t ldy;
 };
 
-// The tile's expert and rows. Tiles are counted expert by expert, ceil(rows / BM)
-// each; every wave finds the tile by itself from the offsets, 64 experts at a
-// time. Offsets are clamped to [0, M], so a damaged list stays in range.
-// Returns false when there is no such tile.
+// Rows of expert e. Offsets are clamped to [0, M], so a damaged list stays in range.
+__device__ __forceinline__ void expert_rows(const Int8Args& p, int e, int* lo, int* hi) {
+    *lo = *hi = 0;
+    if (e < p.E) {
+        *lo = min(max(p.offsets[e], 0), p.M);
+        *hi = min(max(p.offsets[e + 1], *lo), p.M);
+    }
+}
+
+// Tiles are counted expert by expert, ceil(rows / BM) each. The host knows only
+// their largest number, so every wave counts them, 64 experts at a time.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const Int8Args& p, int lane) {
+    if (!p.offsets) return (p.M + BM - 1) / BM;
+    int n = 0;
+    for (int base = 0; base < p.E; base += 64) {
+        int lo, hi;
+        expert_rows(p, base + lane, &lo, &hi);
+        n += (hi - lo + BM - 1) / BM;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// The tile's expert and rows; false when there is no such tile.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const Int8Args& p, int tile, int lane, int* e_out, int* row0, int* rows) {
     if (!p.offsets) {
@@ -95,91 +123,558 @@ __device__ __forceinline__ bool find_tile(const Int8Args& p, int tile, int lane,
     }
     int before = 0;
     for (int base = 0; base < p.E; base += 64) {
-        const int e = base + lane;
-        int lo = 0, hi = 0;
-        if (e < p.E) {
-            lo = min(max(p.offsets[e], 0), p.M);
-            hi = min(max(p.offsets[e + 1], lo), p.M);
-        }
+        int lo, hi;
+        expert_rows(p, base + lane, &lo, &hi);
         const int n = (hi - lo + BM - 1) / BM;
-        int incl = n;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(incl, off);
-            if (lane >= off) incl += v;
-        }
+        const int incl = wave_incl_scan(n);
         const int excl = before + incl - n;
         const uint64_t hit = __ballot(tile >= excl && tile < excl + n);
         if (hit) {
             const int src = __ffsll((unsigned long long)hit) - 1;
-            const int first = __shfl(lo, src) + (tile - __shfl(excl, src)) * BM;
+            const int first = __builtin_amdgcn_readlane(lo, src) + (tile - __builtin_amdgcn_readlane(excl, src)) * BM;
             *e_out = base + src;
             *row0 = first;
-            *rows = min(BM, __shfl(hi, src) - first);
+            *rows = min(BM, __builtin_amdgcn_readlane(hi, src) - first);
             return true;
         }
-        before += __shfl(incl, 63);
+        before += __builtin_amdgcn_readlane(incl, 63);
     }
     return false;
 }
 
-// 64 x 64 tiles of four waves, 64 bytes of depth a step, both operands through
-// the LDS.
-template <typename T>
-__global__ __launch_bounds__(256) void int8_matmul_kernel(Int8Args p) {
-    constexpr int BM = 64, BN = 64, LD = 64 + 16;
-    __shared__ __attribute__((aligned(16))) int8_t sA[BM * LD], sB[BN * LD];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int e, row0, rows;
-    if (!find_tile<BM>(p, blockIdx.x, lane, &e, &row0, &rows)) return;
-    const int n0 = blockIdx.y * BN;
-    const int r = tid >> 2, kc = (tid & 3) * 16;
-    int arow = -1;
-    if (r < rows) {
-        arow = row0 + r;
-        if (p.row_to_route) arow = p.row_to_route[row0 + r] / p.topk;
-        if ((uint32_t)arow >= (uint32_t)p.a_rows) arow = -1;
-    }
-    const int brow = n0 + r < p.N ? n0 + r : -1;
-    i32x4 acc[4] = {};
-    for (int k = 0; k < p.Kd; k += 64) {
-        uint4 av = make_uint4(0, 0, 0, 0), bv = av;
-        if (k + kc < p.Kd) {
-            if (arow >= 0) av = *reinterpret_cast<const uint4*>(p.a + (int64_t)arow * p.lda + k + kc);
-            if (brow >= 0) bv = *reinterpret_cast<const uint4*>(p.b + (int64_t)e * p.b_expert + (int64_t)brow * p.ldb + k + kc);
-        }
-        __syncthreads();
-        *reinterpret_cast<uint4*>(&sA[r * LD + kc]) = av;
-        *reinterpret_cast<uint4*>(&sB[r * LD + kc]) = bv;
-        __syncthreads();
-        const i32x4 bf = *reinterpret_cast<const i32x4*>(&sB[(wave * 16 + (lane & 15)) * LD + 16 * (lane >> 4)]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const i32x4 af = *reinterpret_cast<const i32x4*>(&sA[(i * 16 + (lane & 15)) * LD + 16 * (lane >> 4)]);
-            acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af, bf, acc[i], 0, 0, 0);
-        }
-    }
-    const int n = n0 + wave * 16 + (lane & 15);
-    if (n >= p.N) return;
-    const float sb = p.sb[(size_t)e * p.N + n], bias = p.bias ? p.bias[(size_t)e * p.N + n] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = i * 16 + 4 * (lane >> 4) + j;
-            if (m >= rows) continue;
-            int ar = row0 + m;
-            if (p.row_to_route) ar = p.row_to_route[row0 + m] / p.topk;
-            if ((uint32_t)ar >= (uint32_t)p.a_rows) continue;
-            const float v = __fmaf_rn((float)acc[i][j] * p.sa[ar], sb, bias);
-            static_cast<T*>(p.y)[(int64_t)(row0 + m) * p.ldy + n] = from_f32<T>(v);
-        }
+// ---------------------------------------------------------------------------
+// wide tiles
+// ---------------------------------------------------------------------------
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+template <typename T, int N>
+struct __attribute__((packed, aligned(sizeof(T)))) Few {
+    T e[N];
+};
+
+// Direct buffer -> LDS load of 16 bytes per lane from `base` + `off` (zeros from
+// `bytes` on): lane l's bytes land at dst + 16 l (dst is uniform across the wave).
+__device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t bytes, uint32_t off, void* dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000),
+                                             (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
 }
 
+// s_waitcnt until no vector-memory and no LDS operation of this wave is
+// outstanding, then the workgroup barrier.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The workgroup barrier once this wave's LDS operations are done (loads into the
+// LDS may still be on their way).
+__device__ __forceinline__ void wait_lds_and_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Stores N consecutive results of one row past the caches (nothing reads them here
+// again; with normal stores they push rows of A and B out of the L2: 16384 x 4096 x
+// 7168 went from 454 to 437 us, 98304 x 2048 x 2048 in 64 groups from 525 to 482).
+template <typename T, int N>
+__device__ __forceinline__ void store_past_caches(T* dst, const Few<T, N>& v) {
+    typedef uint32_t words4 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef uint32_t words2 __attribute__((ext_vector_type(2), aligned(2)));
+    constexpr int B = N * (int)sizeof(T);
+    static_assert(B % 8 == 0, "whole stores");
+    const char* src = reinterpret_cast<const char*>(&v);
+    char* to = reinterpret_cast<char*>(dst);
+#pragma unroll
+    for (int i = 0; i + 16 <= B; i += 16)
+        __builtin_nontemporal_store(*reinterpret_cast<const words4*>(src + i), reinterpret_cast<words4*>(to + i));
+    if constexpr (B % 16)
+        __builtin_nontemporal_store(*reinterpret_cast<const words2*>(src + B - 8), reinterpret_cast<words2*>(to + B - 8));
+}
+
+// Until this wave's loads (and stores) are done.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Byte offset that lies behind every buffer (their extents are checked on the
+// host to be at most this): loads there return zeros.
+constexpr uint32_t kOutOfRange = 0xFFFF0000u;
+
+// One block per CU walks tiles of BM x BN (BM rows of one expert); NW = WM * WN
+// waves of ME * 16 rows x NT * 16 columns each (row group g of the tile belongs to
+// wave row g % WM, so that an expert's last, partly filled tile shortens every
+// wave's work: the products run over ME = MT, MT / 2 or MT / 4 groups).
+//  - A and B go through S LDS buffers of 128 bytes of depth, filled by direct
+//    loads of whole 128-byte lines.
+//  - The first S steps of the next tile are requested between a tile's last step
+//    and its epilogue.
+template <typename T, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int ntiles) {
+    constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
+    constexpr int BK = 128, SL = BK / 64;               // bytes of depth per step, slices per step
+    constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // 1 KB loads of A and of B per wave and step
+    constexpr int L = LA + LB, BUF = (BM + BN) * BK;
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && MT >= 1 && BM <= NW * 64 && BN <= NW * 64, "tile shape");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S * BUF];
+    __shared__ int s_first[kMaxE];   // grouped: tiles of the lower experts
+    __shared__ int s_arow[2][BM];    // row of A of each row of the tile, -1 for none
+    __shared__ __attribute__((aligned(16))) float s_sa[2][BM], s_sb[2][BN], s_bias[2][BN];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+
+    int mtiles = (p.M + BM - 1) / BM;
+    if (p.offsets) {  // every wave writes the same list
+        mtiles = 0;
+        for (int base = 0; base < p.E; base += 64) {
+            int lo, hi;
+            expert_rows(p, base + lane, &lo, &hi);
+            const int n = (hi - lo + BM - 1) / BM;
+            const int incl = wave_incl_scan(n);
+            if (base + lane < p.E) s_first[base + lane] = mtiles + incl - n;
+            mtiles += __builtin_amdgcn_readlane(incl, 63);
+        }
+    }
+    // Tile order: one contiguous range per XCD (blocks are dealt to the 8 XCDs in
+    // turn), dealt to the XCD's blocks in turn. Inside it expert by expert, and there
+    // groups of 8 M-tiles walk the N-blocks together: the tiles an XCD works on at a
+    // time share rows of B (and of A) in its L2.
+    constexpr int GM = 8;
+    const int per = (mtiles * ntiles + 7) >> 3;
+    const int last = min((int)(blockIdx.x & 7) * per + per, mtiles * ntiles);
+    int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int stride = gridDim.x >> 3;
+
+    struct Tile {
+        int e, row0, rows, n0, cols;
+    };
+    auto locate = [&](int i) {
+        Tile t;
+        int lo = 0, hi = p.M;
+        t.e = 0;
+        if (p.offsets) {
+            int cnt = 0;  // the last expert whose first tile is not behind i (an empty one has the next one's)
+            for (int base = 0; base < p.E; base += 64)
+                cnt += __popcll(__ballot(base + lane < p.E && s_first[base + lane] * ntiles <= i));
+            t.e = cnt - 1;
+            i -= s_first[t.e] * ntiles;
+            // (the constant address space: scalar loads, which do not wait for this wave's stores)
+            const auto* off = (const __attribute__((address_space(4))) int32_t*)p.offsets;
+            const int e = __builtin_amdgcn_readfirstlane(t.e);
+            lo = min(max(off[e], 0), p.M);
+            hi = min(max(off[e + 1], lo), p.M);
+        }
+        const int tiles = (hi - lo + BM - 1) / BM;
+        const int group = i / (GM * ntiles), in = i - group * GM * ntiles;
+        const int gm = min(GM, tiles - group * GM);
+        const int nb = in / gm, mt = group * GM + in - nb * gm;
+        t.n0 = nb * BN;
+        t.cols = min(BN, p.N - t.n0);
+        t.e = __builtin_amdgcn_readfirstlane(t.e);
+        t.row0 = __builtin_amdgcn_readfirstlane(lo + mt * BM);
+        t.rows = __builtin_amdgcn_readfirstlane(min(BM, hi - lo - mt * BM));
+        return t;
+    };
+    // Thread r < BM looks up row r of the tile: first the route, later the row of A
+    // and its scale (rows behind the tile's last repeat its first).
+    auto route_of_row = [&](const Tile& t) {
+        int r = 0;
+        if (tid < BM) {
+            r = t.row0 + (tid < t.rows ? tid : 0);
+            if (p.row_to_route) r = p.row_to_route[r];
+        }
+        return r;
+    };
+    auto row_of_route = [&](int r) {
+        const int ar = p.row_to_route ? r / p.topk : r;
+        return r >= 0 && ar < p.a_rows ? ar : -1;
+    };
+
+    // Staging: one load brings 8 rows of 128 bytes; lane l lands at byte 16 l of its
+    // 1 KB, i.e. in slot l % 8 of row l / 8, and fetches chunk (l % 8) ^ mix(row). The
+    // LDS serves 16 lanes of an operand read (one chunk of 16 rows) at a time over 256
+    // bytes of banks: every second row has the same banks, and mix() gives the eight
+    // of them another slot each. An operand of A has rows 0 .. 15 of its group; one of
+    // B, number j, rows CQ q + 4 j + c (q, c < 4) of its wave's 4 CQ: a lane then
+    // ends up with CQ consecutive columns of the result.
+    constexpr int CQ = 4 * NT;
+    auto mix_a = [](int row) { return (row >> 1) & 7; };
+    auto mix_b = [](int row) { return ((row / CQ) & 3) * 2 + ((row >> 1) & 1); };
+    const int lr = lane >> 3;
+    auto chunk_a = [&](int i) { return ((lane & 7) ^ mix_a((wave + NW * i) * 8 + lr)) << 4; };  // of the wave's load i
+    auto chunk_b = [&](int i) { return ((lane & 7) ^ mix_b((wave + NW * i) * 8 + lr)) << 4; };
+    const int KT = (p.Kd + BK - 1) / BK;
+    const int8_t *abase, *bbase;
+    uint32_t a_bytes, b_bytes, aoff[LA], boff[LB];
+    auto address = [&](const Tile& t, int par) {
+        abase = p.row_to_route ? p.a : p.a + (int64_t)t.row0 * p.lda;
+        bbase = p.b + (int64_t)t.e * p.b_expert + (int64_t)t.n0 * p.ldb;
+        a_bytes = (uint32_t)((int64_t)((p.row_to_route ? p.a_rows : t.rows) - 1) * p.lda + p.Kd);
+        b_bytes = (uint32_t)((int64_t)(t.cols - 1) * p.ldb + p.Kd);
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            const int ar = max(s_arow[par][(wave + NW * i) * 8 + lr], 0) - (p.row_to_route ? 0 : t.row0);
+            aoff[i] = (uint32_t)ar * (uint32_t)p.lda + chunk_a(i);
+        }
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+            boff[i] = (uint32_t)min((wave + NW * i) * 8 + lr, t.cols - 1) * (uint32_t)p.ldb + chunk_b(i);
+    };
+    auto issue = [&](int kt, int buf) {
+        const int k = kt * BK;
+        // the last step of a depth that is no multiple of 128: chunks behind the row's
+        // end take an offset that the buffer's range check answers with zeros
+        const int left = p.Kd - k;
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            buffer_load_lds16(abase, a_bytes, left < BK && chunk_a(i) >= left ? kOutOfRange : aoff[i] + (uint32_t)k,
+                              lds + buf * BUF + (wave + NW * i) * 1024);
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+            buffer_load_lds16(bbase, b_bytes, left < BK && chunk_b(i) >= left ? kOutOfRange : boff[i] + (uint32_t)k,
+                              lds + buf * BUF + BM * BK + (wave + NW * i) * 1024);
+    };
+    auto issue_first = [&]() {
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+            if (u < KT) issue(u, u);
+    };
+
+    if (id >= last) return;
+    __syncthreads();
+    Tile t = locate(id), nt = t;
+    int par = 0;
+    float my_sa = 0.0f, my_sb = 0.0f, my_bias = 0.0f;
+    // Row r < BM of a tile and column c < BN belong to thread r, c: row of A, scales, bias.
+    auto look_up = [&](const Tile& t, int route, int par) {
+        if (tid < BM) {
+            const int ar = row_of_route(route);
+            s_arow[par][tid] = ar;
+            my_sa = p.sa[max(ar, 0)];
+        }
+        if (tid < t.cols) {
+            const size_t ne = (size_t)t.e * p.N + t.n0 + tid;
+            my_sb = p.sb[ne];
+            if (p.bias) my_bias = p.bias[ne];
+        }
+    };
+    look_up(t, route_of_row(t), 0);
+    __syncthreads();
+    address(t, 0);
+    issue_first();
+    wait_loads();
+
+    // Operands of 16 rows x 64 bytes: lane l holds row l % 16, chunk 4 s + l / 16 of slice s.
+    const int r16 = lane & 15, quad = lane >> 4;
+    const int b_row = wn * NT * 16 + CQ * (r16 >> 2) + (r16 & 3);  // of operand 0
+    const int a_at = (wm * 16 + r16) * BK, b_at = BM * BK + b_row * BK;
+    const int slot_a = (quad ^ mix_a(r16)) << 4, slot_b = (quad ^ mix_b(b_row)) << 4;
+    T* const y = static_cast<T*>(p.y);
+    bool more;
+
+    auto tile = [&](auto me_tag, int next_route) {
+        constexpr int ME = decltype(me_tag)::value;
+        // A slice's rows of A come in H parts of HM groups, which bounds the operands held
+        constexpr int HM = ME > 4 ? 4 : ME, H = ME / HM, UNITS = SL * H;
+        i32x4 fa[2][HM], fb[2][NT];
+        auto fetch_b = [&](int buf, int sl) {
+            const int o = buf * BUF + (slot_b ^ (sl << 6)) + b_at;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) fb[sl & 1][j] = *reinterpret_cast<const i32x4*>(&lds[o + j * 4 * BK]);
+        };
+        auto fetch_a = [&](int buf, int sl, int h) {
+            const int o = buf * BUF + (slot_a ^ (sl << 6)) + a_at;
+#pragma unroll
+            for (int i = 0; i < HM; ++i)
+                fa[(sl * H + h) & 1][i] = *reinterpret_cast<const i32x4*>(&lds[o + (h * HM + i) * WM * 16 * BK]);
+        };
+        i32x4 acc[NT][ME];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < ME; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+
+        // One barrier per step: at the end of step kt every wave has read its last
+        // operands from the step's buffer and its loads of step kt + 1 have landed, so
+        // behind the barrier the loads of step kt + S may overwrite the one while the
+        // first operands come from the next; the last products cover both.
+        static_assert(UNITS % 2 == 0 && SL % 2 == 0, "operand buffers alternate across steps");
+        fetch_b(0, 0);
+        fetch_a(0, 0, 0);
+        int buf = 0;
+        for (int kt = 0; kt < KT; ++kt) {
+            const int next = buf + 1 == S ? 0 : buf + 1;
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const int sl = u / H, h = u % H;
+                if (u + 1 == UNITS) {
+                    if (kt + S <= KT) wait_and_barrier<(S - 2) * L>();
+                    else wait_and_barrier<0>();
+                    if (kt + 1 < KT) {
+                        fetch_b(next, 0);
+                        fetch_a(next, 0, 0);
+                    }
+                    if (kt + S < KT) issue(kt + S, buf);
+                } else if (h + 1 < H) {
+                    fetch_a(buf, sl, h + 1);
+                } else {
+                    fetch_b(buf, sl + 1);
+                    fetch_a(buf, sl + 1, 0);
+                }
+                // B in the place of the left operand: a lane then holds four consecutive
+                // columns of one row of the result. (16x16x64: register-only loops over
+                // normal data reach 4.0 POP/s of it and 3.4 of 32x32x32, at the power limit.)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < HM; ++i)
+                        acc[j][h * HM + i] =
+                            __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[sl & 1][j], fa[u & 1][i], acc[j][h * HM + i], 0, 0, 0);
+            }
+            buf = next;
+        }
+
+        // every wave has read its last operands (the last step's barrier): the next
+        // tile's loads may start
+        if (more) {
+            look_up(nt, next_route, par ^ 1);
+            wait_lds_and_barrier();
+            address(nt, par ^ 1);
+            issue_first();
+        }
+
+        // acc[j][i][c]: row (i*WM + wm)*16 + lane % 16, column CQ (lane / 16) + 4 j + c
+        float sa[ME];
+        bool ok[ME];
+#pragma unroll
+        for (int i = 0; i < ME; ++i) {
+            const int m = (i * WM + wm) * 16 + r16;
+            ok[i] = m < t.rows && s_arow[par][m] >= 0;
+            sa[i] = s_sa[par][m];
+        }
+        const int col = wn * NT * 16 + CQ * quad, n = t.n0 + col, left = p.N - n;
+        Few<T, CQ> o[ME];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const f32x4 sb = *reinterpret_cast<const f32x4*>(&s_sb[par][col + 4 * j]);
+            f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (p.bias) bias = *reinterpret_cast<const f32x4*>(&s_bias[par][col + 4 * j]);
+#pragma unroll
+            for (int i = 0; i < ME; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    o[i].e[4 * j + c] = from_f32<T>(__fmaf_rn((float)acc[j][i][c] * sa[i], sb[c], bias[c]));
+        }
+        // the next tile's first steps have landed before any store is on its way, so
+        // that no wait at the tile's start has to wait for stores
+        wait_loads();
+#pragma unroll
+        for (int i = 0; i < ME; ++i) {
+            if (!ok[i]) continue;
+            T* dst = y + (int64_t)(t.row0 + (i * WM + wm) * 16 + r16) * p.ldy + n;
+            if (left >= CQ) {
+                store_past_caches<T, CQ>(dst, o[i]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < CQ - 1; ++c)
+                    if (c < left) dst[c] = o[i].e[c];
+            }
+        }
+    };
+
+    for (;;) {
+        if (tid < BM) s_sa[par][tid] = my_sa;
+        if (tid < BN) {
+            s_sb[par][tid] = my_sb;
+            s_bias[par][tid] = my_bias;
+        }
+        wait_lds_and_barrier();  // every wave's share of the tile's first steps has landed
+        id += stride;
+        more = id < last;
+        int next_route = 0;
+        if (more) {
+            nt = locate(id);
+            next_route = route_of_row(nt);  // consumed after the main loop
+        }
+        if (MT < 2 || t.rows > BM / 2) tile(std::integral_constant<int, MT>{}, next_route);
+        else if (MT < 4 || t.rows > BM / 4) tile(std::integral_constant<int, (MT + 1) / 2>{}, next_route);
+        else tile(std::integral_constant<int, (MT + 3) / 4>{}, next_route);
+        if (!more) break;
+        t = nt;
+        par ^= 1;
+    }
+}
+
+// CUs of the current device (0 if the runtime cannot say), asked once per device.
+static int cu_count() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+    int c = cache[dev].load(std::memory_order_relaxed);
+    if (c == 0) {
+        if (hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+        cache[dev].store(c, std::memory_order_relaxed);
+    }
+    return c;
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int S>
+static void launch_wide(const Int8Args& p, hipStream_t s) {
+    const int64_t mtiles = (p.M + BM - 1) / BM + (p.offsets ? p.E : 0), ntiles = (p.N + BN - 1) / BN;
+    const int64_t blocks = std::min<int64_t>(std::max(cu_count(), 8), mtiles * ntiles);
+    hipLaunchKernelGGL((int8_wide_kernel<T, BM, BN, WM, WN, S>), dim3((unsigned)((blocks + 7) / 8 * 8)),
+                       dim3(WM * WN * 64), 0, s, p, (int)ntiles);
+}
+
+// ---------------------------------------------------------------------------
+// narrow tiles
+// ---------------------------------------------------------------------------
+// MS * 16 rows x NS * 16 columns per block, for few rows (where B's bytes are
+// what counts) and small products (where latency is). The depth is dealt to the
+// block's NW waves, 128 bytes at a time, each wave keeps P such pieces of both
+// operands on their way straight into its registers, and the waves' integer sums
+// are joined through the LDS, which is exact in any order.
+template <typename T, int MS, int NS, int NW, int P>
+__global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int ntiles) {
+    constexpr int BM = MS * 16, BN = NS * 16;
+    __shared__ __attribute__((aligned(16))) i32x4 part[NW][MS * NS][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, quad = lane >> 4;
+    // one contiguous range of tiles per XCD, M-tiles of a column block side by side
+    const int mtiles = count_tiles<BM>(p, lane);
+    const int per = (int)(((int64_t)mtiles * ntiles + 7) >> 3), j8 = blockIdx.x >> 3;
+    const int id = (blockIdx.x & 7) * per + j8;
+    if (j8 >= per || id >= mtiles * ntiles) return;
+    int e, row0, rows;
+    if (!find_tile<BM>(p, id % mtiles, lane, &e, &row0, &rows)) return;
+    const int n0 = id / mtiles * BN;
+
+    const int8_t *ap[MS], *bp[NS];
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+        int ar = row0 + min(i * 16 + r16, rows - 1);
+        if (p.row_to_route) {
+            ar = p.row_to_route[ar] / p.topk;
+            ar = (uint32_t)ar < (uint32_t)p.a_rows ? ar : 0;
+        }
+        ap[i] = p.a + (int64_t)ar * p.lda + quad * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+        bp[j] = p.b + (int64_t)e * p.b_expert + (int64_t)min(n0 + j * 16 + r16, p.N - 1) * p.ldb + quad * 16;
+
+    i32x4 fa[P][2][MS], fb[P][2][NS];
+    i32x4 acc[NS][MS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int i = 0; i < MS; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+    auto load = [&](int st, int k) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const bool in = k + s * 64 + quad * 16 < p.Kd;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                fb[st][s][j] = in ? __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(bp[j] + k + s * 64)) : i32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+                fa[st][s][i] = in ? *reinterpret_cast<const i32x4*>(ap[i] + k + s * 64) : i32x4{0, 0, 0, 0};
+        }
+    };
+    auto multiply = [&](int st) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < MS; ++i)
+                    acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[st][s][j], fa[st][s][i], acc[j][i], 0, 0, 0);
+    };
+    constexpr int STRIDE = NW * 128;
+    int k = wave * 128;
+#pragma unroll
+    for (int u = 0; u < P; ++u) load(u, k + u * STRIDE);
+    for (; k < p.Kd; k += P * STRIDE) {
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+            multiply(u);
+            load(u, k + (P + u) * STRIDE);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int i = 0; i < MS; ++i) part[wave][j * MS + i][lane] = acc[j][i];
+    __syncthreads();
+    // part[w][j * MS + i][lane][c]: row i * 16 + lane % 16, column j * 16 + 4 (lane / 16) + c
+    T* const y = static_cast<T*>(p.y);
+    for (int f = wave; f < MS * NS; f += NW) {
+        i32x4 sum = part[0][f][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) sum += part[w][f][lane];
+        const int m = (f % MS) * 16 + r16, n = n0 + (f / MS) * 16 + 4 * quad, left = p.N - n;
+        if (m >= rows || left <= 0) continue;
+        int ar = row0 + m;
+        if (p.row_to_route) ar = p.row_to_route[ar] / p.topk;
+        if ((uint32_t)ar >= (uint32_t)p.a_rows) continue;
+        const float sa = p.sa[ar];
+        const size_t ne = (size_t)e * p.N + n;
+        T* dst = y + (int64_t)(row0 + m) * p.ldy + n;
+        Few<T, 4> o;
+        if (left >= 4) {
+            const Few<float, 4> sb = *reinterpret_cast<const Few<float, 4>*>(p.sb + ne);
+            Few<float, 4> bias = {};
+            if (p.bias) bias = *reinterpret_cast<const Few<float, 4>*>(p.bias + ne);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o.e[c] = from_f32<T>(__fmaf_rn((float)sum[c] * sa, sb.e[c], bias.e[c]));
+            *reinterpret_cast<Few<T, 4>*>(dst) = o;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+                if (c < left) dst[c] = from_f32<T>(__fmaf_rn((float)sum[c] * sa, p.sb[ne + c], p.bias ? p.bias[ne + c] : 0.0f));
+        }
+    }
+}
+
+template <typename T, int MS, int NS, int NW, int P>
+static void launch_narrow(const Int8Args& p, hipStream_t s) {
+    const int64_t mtiles = (p.M + MS * 16 - 1) / (MS * 16) + (p.offsets ? p.E : 0), ntiles = (p.N + NS * 16 - 1) / (NS * 16);
+    hipLaunchKernelGGL((int8_narrow_kernel<T, MS, NS, NW, P>), dim3((unsigned)((mtiles * ntiles + 7) / 8 * 8)),
+                       dim3(NW * 64), 0, s, p, (int)ntiles);
+}
+
+// The tile shape: the largest that still gives about one block per CU. A larger
+// tile moves fewer bytes per product, but a product that does not fill the CUs is
+// bound by the time of one block. Columns N = 4096, depth 7168, bf16, in us:
+//   rows      256x256  128x256  128x128  64x128  64x32  32x32  16x32  16x16
+//   16384         437      507
+//    2048          92       65       79
+//    1024          91       57       44      59
+//     512          91       56       40      32     92
+//     256          90       56       39      31     50
+//     128          63       56       39      30     27     35
+//      64                             29      30     28     20     26
+//      32                             26             22     21     16     19
+//      16                             26             19     18     17     14
+// For experts the host knows the mean rows only: 64 tokens with 8 of 256 experts,
+// depth 7168: 758 us with 128x256 (6.0 TB/s of weights), 1044 or more with 16 rows;
+// 256-row tiles pay from about 192 mean rows on (128: 576 against 521 us, 1536: 482
+// against 528). A single token's broadcast rows cost the narrow tiles nothing:
+// 28672 x 8192 takes 49 us with 16x16 and 52 with 128x128; with 16 rows it is 71
+// and 53.
 template <typename T>
 static hipError_t launch_int8_matmul(const Int8Args& p, hipStream_t s) {
-    const int tiles = (p.M + 63) / 64 + (p.offsets ? p.E : 0);
-    hipLaunchKernelGGL(int8_matmul_kernel<T>, dim3(tiles, (p.N + 63) / 64), dim3(256), 0, s, p);
+    const int64_t groups = p.offsets ? std::min(p.E, p.M) : 1;
+    const int64_t mean = (p.M + groups - 1) / groups;
+    auto blocks = [&](int bm, int bn) { return groups * ((mean + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
+    const int64_t cus = std::max(cu_count(), 8), full = cus * 7 / 8;
+    const bool one = !p.offsets && p.M <= 4;
+    if (!one && mean >= 192 && blocks(256, 256) >= full) launch_wide<T, 256, 256, 2, 4, 2>(p, s);
+    else if (!one && blocks(128, 256) >= full) launch_wide<T, 128, 256, 2, 4, 3>(p, s);
+    else if (!one && blocks(128, 128) >= full) launch_wide<T, 128, 128, 2, 4, 4>(p, s);
+    else if (!one && blocks(64, 128) >= cus * 3 / 8) launch_wide<T, 64, 128, 1, 8, 5>(p, s);
+    else if (!one && blocks(64, 32) >= full) launch_narrow<T, 4, 2, 8, 2>(p, s);
+    else if (!one && blocks(32, 32) >= full) launch_narrow<T, 2, 2, 8, 3>(p, s);
+    else if (!one && blocks(16, 32) >= full) launch_narrow<T, 1, 2, 8, 3>(p, s);
+    else launch_narrow<T, 1, 1, 8, 4>(p, s);
     return hipGetLastError();
 }
 
@@ -203,8 +698,13 @@ static int run_int8_matmul(Int8Args p, int out_dtype, bool grouped, hipStream_t 
     if ((p.a_rows > 1 && p.lda < p.Kd) || (p.N > 1 && p.ldb < p.Kd) || (p.M > 1 && p.ldy < p.N) ||
         (grouped && p.E > 1 && p.b_expert < 0))
         return reject(MOE_ERR_INVALID, "a row stride is below the row");
-    const int64_t far = (int64_t)1 << 31;
-    if (p.lda > far || p.ldb > far || p.ldy > far) return reject(MOE_ERR_UNSUPPORTED, "a row stride above 2^31");
+    const int64_t far = (int64_t)1 << 23;  // 256 rows of a tile are addressed by 32-bit offsets
+    if ((p.a_rows > 1 && p.lda > far) || (p.N > 1 && p.ldb > far) || (p.M > 1 && p.ldy > ((int64_t)1 << 31)))
+        return reject(MOE_ERR_UNSUPPORTED, "a row stride above 2^23 bytes (a, b) or 2^31 elements (y)");
+    if (p.row_to_route && extent(p.a_rows, p.lda, p.Kd, 1) > kOutOfRange)
+        return reject(MOE_ERR_UNSUPPORTED, "gathered rows of 4 GiB or more");
+    const int64_t most = ((int64_t)(p.M + 15) / 16 + (grouped ? p.E : 0)) * ((p.N + 15) / 16);
+    if (most >= ((int64_t)1 << 31)) return reject(MOE_ERR_UNSUPPORTED, "M=%d, N=%d: too many tiles", p.M, p.N);
     if ((p.a_rows > 1 && p.lda % 16) || (p.N > 1 && p.ldb % 16) || (grouped && p.E > 1 && p.b_expert % 16))
         return reject(MOE_ERR_UNSUPPORTED, "the strides of a and b must be multiples of 16");
     const size_t es = dtype_bytes(out_dtype);

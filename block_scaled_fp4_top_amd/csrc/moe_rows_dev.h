@@ -11,11 +11,10 @@ struct Fp16 { _Float16 v; };
 __device__ __forceinline__ float to_f32(Bf16 x) { return u2f((uint32_t)x.v << 16); }
 __device__ __forceinline__ float to_f32(Fp16 x) { return (float)x.v; }
 __device__ __forceinline__ float to_f32(float x) { return x; }
-// round to nearest even; a NaN stays one (the integer rounding of bf16_rne
-// would carry a NaN's payload into its sign)
+// round to nearest even by the hardware converters (a NaN stays one)
 template <typename T> __device__ __forceinline__ T from_f32(float f);
 template <> __device__ __forceinline__ Bf16 from_f32<Bf16>(float f) {
-    return Bf16{f == f ? bf16_rne(f) : (uint16_t)((f2u(f) >> 16) | 0x40u)};
+    return Bf16{__builtin_bit_cast(uint16_t, (__bf16)f)};
 }
 template <> __device__ __forceinline__ Fp16 from_f32<Fp16>(float f) { return Fp16{(_Float16)f}; }
 template <> __device__ __forceinline__ float from_f32<float>(float f) { return f; }

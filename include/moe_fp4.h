@@ -299,7 +299,8 @@ int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, int32_t row
  * integer sums, scales and bias in fp32, one rounding to out_dtype (moe_dtype).
  *   a: [M][K], b: [N][K] int8, 16-byte aligned with strides that are multiples
  *   of 16; bias: [N] fp32 or NULL; y: [M][N].  K a multiple of 16 below 131072
- *   (MOE_ERR_UNSUPPORTED otherwise), N <= 2^20, M <= 2^26. */
+ *   (MOE_ERR_UNSUPPORTED otherwise, as for strides of a and b above 2^23, N above
+ *   2^20 and M above 2^26). */
 int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, const int8_t* b,
                    int64_t b_stride, const float* b_scales, const float* bias, int32_t M, int32_t N,
                    int32_t K, int32_t out_dtype, void* y, int64_t y_stride, hipStream_t stream);
@@ -310,8 +311,8 @@ int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, con
  * the offsets are left as they were.
  *   row_to_route NULL: row r of y uses row r of a (a_rows = M).
  *   Otherwise row r uses row row_to_route[r] / topk of a, the token's (a_rows =
- *   M / topk tokens): FC1 needs no dispatched copy. Rows whose entry names no
- *   token are left as they were. */
+ *   M / topk tokens, below 4 GiB): FC1 needs no dispatched copy. Rows whose
+ *   entry names no token are left as they were. */
 int moe_int_grouped_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, int32_t a_rows,
                            const int8_t* b, int64_t b_stride, int64_t b_expert_stride,
                            const float* b_scales, const float* bias, const int32_t* offsets,

@@ -307,7 +307,11 @@ def pad_codes(a, pad):
 
 MATMULS = [(1, 1, 16), (1, 17, 32), (1, 4096, 512), (2, 16, 48), (3, 300, 64), (15, 64, 80), (16, 256, 128), (17, 130, 144),
            (31, 33, 2064), (33, 512, 256), (64, 100, 1008), (65, 257, 272), (128, 128, 128), (129, 255, 512), (200, 640, 2048),
-           (257, 513, 400), (300, 1024, 1024), (513, 777, 176), (1000, 520, 640), (1025, 1100, 336)]
+           (257, 513, 400), (300, 1024, 1024), (513, 777, 176), (1000, 520, 640), (1025, 1100, 336),
+           # every tile shape on a chip of 256 CUs, with ragged edges: 16x32, 32x32, 64x32, 64x128, 128x128, 128x256
+           # and 256x256, depths of one step, of several and with a cut last step
+           (16, 7200, 272), (30, 7190, 656), (60, 7201, 144), (300, 2601, 304), (301, 2602, 1296), (1000, 3603, 16),
+           (999, 3601, 400), (1801, 4002, 128), (1799, 4001, 272), (4000, 3702, 176), (3851, 3841, 256), (3999, 3701, 528)]
 
 
 @pytest.mark.parametrize("dtype", DT, ids=NAME.get)
@@ -348,7 +352,10 @@ GROUPED = [  # T, K, N, depth, E, drop, skew
     (1, 1, 16, 16, 1, False, False), (1, 8, 96, 64, 32, False, False), (7, 2, 33, 48, 5, True, False),
     (64, 8, 256, 512, 64, False, False), (40, 3, 130, 144, 16, True, True), (100, 8, 512, 256, 4, False, False),
     (300, 4, 260, 208, 8, True, False), (513, 2, 192, 128, 3, False, True), (600, 8, 640, 384, 12, True, False),
-    (128, 1, 64, 2048, 100, False, False), (9, 64, 48, 32, 7, True, False), (700, 6, 257, 1040, 2, False, False)]
+    (128, 1, 64, 2048, 100, False, False), (9, 64, 48, 32, 7, True, False), (700, 6, 257, 1040, 2, False, False),
+    # the wide tiles: 64x128, 128x128, 128x256 (many and few rows), 256x256, with empty and ragged groups
+    (90, 6, 1301, 208, 10, True, False), (160, 6, 1902, 336, 16, True, True), (300, 4, 3003, 144, 20, False, False),
+    (40, 8, 2050, 272, 60, False, True), (1200, 4, 2403, 208, 12, False, False), (1100, 4, 2302, 400, 12, True, True)]
 
 
 @pytest.mark.parametrize("dtype", DT, ids=NAME.get)
