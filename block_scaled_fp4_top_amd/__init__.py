@@ -333,7 +333,7 @@ def _on_stream(f):
             raise ValueError("the tensors must be on a GPU")
         dev = first.device
         if stream is None:
-            if dev.index == torch.cuda.current_device():
+            if dev.index == torch._C._cuda_getDevice():
                 return f(*args, **kw)
             with torch.cuda.device(dev):
                 return f(*args, **kw)
@@ -351,7 +351,7 @@ def _on_stream(f):
 
 
 def _raw_stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _matrix(t, name, dtype, device, rows=None, cols=None):
@@ -397,6 +397,12 @@ class RouteOrder:
         for name, n in (("row_to_route", R), ("route_to_row", R), ("offsets", self.E + 1)):
             _need(getattr(self, name), name, torch.int32, (n,), dev)
 
+    @classmethod
+    def _of(cls, *fields):  # of tensors made here: no checks
+        o = object.__new__(cls)
+        o.__dict__.update(zip(("row_to_route", "route_to_row", "offsets", "T", "K", "E"), fields))
+        return o
+
     def tensors(self):
         return self.row_to_route, self.route_to_row, self.offsets
 
@@ -433,14 +439,14 @@ def sort_routes(ids: torch.Tensor, E: int) -> RouteOrder:
     if n == 0:
         raise MoeError(1, _lib.moe_last_error().decode())
     R = T * K
-    # one allocation for the maps and the workspace
-    maps = torch.empty(2 * R + E + 1, dtype=torch.int32, device=ids.device)
-    ws = torch.empty(n, dtype=torch.uint8, device=ids.device)
-    row_to_route, route_to_row, offsets = maps[:R], maps[R:2 * R], maps[2 * R:]
-    _check(_lib.moe_sort_routes(ids.data_ptr(), int(ids.dtype == torch.int64), T, K, E, ws.data_ptr(), n,
-                                row_to_route.data_ptr(), route_to_row.data_ptr(), offsets.data_ptr(),
-                                _raw_stream(ids)))
-    return RouteOrder(row_to_route, route_to_row, offsets, T, K, E)
+    # one allocation: the workspace (whole int32 words), then the maps and the offsets
+    ws = n // 4
+    whole = torch.empty(ws + 2 * R + E + 1, dtype=torch.int32, device=ids.device)
+    p = whole.data_ptr()
+    _check(_lib.moe_sort_routes(ids.data_ptr(), int(ids.dtype == torch.int64), T, K, E, p, n, p + n,
+                                p + n + 4 * R, p + n + 8 * R, _raw_stream(ids)))
+    _, row_to_route, route_to_row, offsets = whole.split_with_sizes((ws, R, R, E + 1))
+    return RouteOrder._of(row_to_route, route_to_row, offsets, T, K, E)
 
 
 @_on_stream

@@ -19,53 +19,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
-// quantizer
-// ---------------------------------------------------------------------------
-// One block per row, two passes. Codes are the correctly rounded quotients
-// x / s of the row's fp32 scale s (ties to even): n = rint(x * (1/s)) is at
-// most one off, and the sign of the exact remainder x - n s (one fma: at most
-// 24 bits remain) against s / 2 decides. A scale that is not finite (a row with
-// an infinity or a NaN) or zero leaves codes 0.
-__device__ __forceinline__ int int8_code(float x, float s, float inv) {
-    float n = __builtin_rintf(x * inv);
-    const float r2 = 2.0f * __fmaf_rn(-n, s, x);  // twice the remainder, exact
-    const bool odd = ((int)n) & 1;
-    if (r2 > s || (r2 == s && odd)) n += 1.0f;
-    else if (r2 < -s || (r2 == -s && odd)) n -= 1.0f;
-    return (int)fminf(fmaxf(n, -127.0f), 127.0f);
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void int8_quantize_kernel(const T* __restrict__ x, int64_t ld, int H,
-                                                            int8_t* __restrict__ codes, int64_t ld_codes,
-                                                            float* __restrict__ scales) {
-    __shared__ uint32_t smax[4];
-    const size_t m = blockIdx.x;
-    const T* row = x + (int64_t)m * ld;
-    // the bits of |x| order like the values, NaN above infinity
-    uint32_t top = 0;
-    for (int i = threadIdx.x; i < H; i += 256) top = max(top, f2u(to_f32(row[i])) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-    if ((threadIdx.x & 63) == 0) smax[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(smax[0], smax[1]), max(smax[2], smax[3]));
-    const float s = __fdiv_rn(u2f(top), 127.0f);
-    const bool zero = !(s > 0.0f) || top >= 0x7F800000u;
-    for (int i = threadIdx.x; i < H; i += 256) {
-        int c = 0;
-        if (!zero) {
-            const float v = to_f32(row[i]);
-            // 1/s overflows below 2^-126: such rows divide in fp64
-            if (s < 1e-37f) c = (int)fmin(fmax(rint((double)v / (double)s), -127.0), 127.0);
-            else c = int8_code(v, s, __fdiv_rn(1.0f, s));
-        }
-        codes[(int64_t)m * ld_codes + i] = (int8_t)c;
-    }
-    if (threadIdx.x == 0) scales[m] = s;
-}
-
-// ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
 struct Int8Args {
@@ -731,28 +684,6 @@ static int run_int8_matmul(Int8Args p, int out_dtype, bool grouped, hipStream_t 
 }  // namespace moe
 
 using namespace moe;
-
-extern "C" int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, int32_t rows, int32_t cols,
-                                int8_t* codes, int64_t codes_stride, float* scales, hipStream_t stream) {
-    if (!dtype_ok(dtype)) return reject(MOE_ERR_INVALID, "dtype=%d is not a moe_dtype", dtype);
-    if (rows < 0) return reject(MOE_ERR_INVALID, "rows=%d is negative", rows);
-    if (cols < 1 || cols > (1 << 20)) return reject(MOE_ERR_UNSUPPORTED, "cols=%d outside [1, %d]", cols, 1 << 20);
-    if (rows == 0) return MOE_OK;
-    if (!x || !codes || !scales) return reject(MOE_ERR_INVALID, "NULL pointer argument");
-    const int64_t far = (int64_t)1 << 32;
-    if (x_stride < 0 || x_stride > far || codes_stride > far || (rows > 1 && codes_stride < cols))
-        return reject(MOE_ERR_INVALID, "row strides %lld and %lld", (long long)x_stride, (long long)codes_stride);
-    const size_t es = dtype_bytes(dtype);
-    if (!is_aligned(x, es) || !is_aligned(scales, 4)) return reject(MOE_ERR_INVALID, "misaligned pointer");
-    const size_t nx = extent(rows, x_stride, cols, (int)es), nc = extent(rows, codes_stride, cols, 1), ns = (size_t)rows * 4;
-    if (overlap(x, nx, codes, nc) || overlap(x, nx, scales, ns) || overlap(codes, nc, scales, ns))
-        return reject(MOE_ERR_INVALID, "buffers overlap");
-    const dim3 grid(rows), block(256);
-    if (dtype == MOE_DT_BF16) hipLaunchKernelGGL(int8_quantize_kernel<Bf16>, grid, block, 0, stream, (const Bf16*)x, x_stride, cols, codes, codes_stride, scales);
-    else if (dtype == MOE_DT_FP16) hipLaunchKernelGGL(int8_quantize_kernel<Fp16>, grid, block, 0, stream, (const Fp16*)x, x_stride, cols, codes, codes_stride, scales);
-    else hipLaunchKernelGGL(int8_quantize_kernel<float>, grid, block, 0, stream, (const float*)x, x_stride, cols, codes, codes_stride, scales);
-    return launched(hipGetLastError(), "8-bit integer quantizer");
-}
 
 extern "C" int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, const int8_t* b,
                               int64_t b_stride, const float* b_scales, const float* bias, int32_t M, int32_t N,

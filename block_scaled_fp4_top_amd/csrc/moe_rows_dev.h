@@ -19,11 +19,24 @@ template <> __device__ __forceinline__ Bf16 from_f32<Bf16>(float f) {
 template <> __device__ __forceinline__ Fp16 from_f32<Fp16>(float f) { return Fp16{(_Float16)f}; }
 template <> __device__ __forceinline__ float from_f32<float>(float f) { return f; }
 
-// 16 bytes of a row at any alignment of its elements (gfx950 loads and stores
-// global memory at any byte address).
+// 16 bytes of a row, read and written in one access at any alignment of its
+// elements (gfx950 takes global memory at any byte address).
 template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Vec {
+struct Vec {
     T e[16 / sizeof(T)];
 };
+typedef uint32_t words4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* p) {
+    const words4_at2 v = *reinterpret_cast<const words4_at2*>(p);
+    return __builtin_bit_cast(Vec<T>, v);
+}
+// PAST: a store that leaves the caches to others.
+template <bool PAST, typename T>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T>& v) {
+    const words4_at2 w = __builtin_bit_cast(words4_at2, v);
+    if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<words4_at2*>(p));
+    else *reinterpret_cast<words4_at2*>(p) = w;
+}
 
 }  // namespace moe

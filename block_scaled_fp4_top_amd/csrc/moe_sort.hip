@@ -63,7 +63,10 @@ __global__ __launch_bounds__(1024) void sort_count_kernel(const ID* __restrict__
 // one block sorts everything). Every block sums the counts of all chunks and of
 // those before its own by itself: that reads nblk * (E + 1) 16-bit values from
 // the L2 and saves a launch for a scan.
-template <typename ID>
+// KEEP: a wave has at most KEEP steps, whose keys and peers it keeps between the
+// two passes; 0: any number, found twice.
+constexpr int kKeep = 4;
+template <typename ID, int KEEP>
 __global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__ ids, int R, int E,
                                                           int chunk, const uint32_t* __restrict__ counts,
                                                           int32_t* __restrict__ row_to_route,
@@ -84,12 +87,28 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__
     // routes per expert of this wave
     const int per = chunk / kSortWaves;
     const long long r0 = (long long)blk * chunk + (long long)wave * per;
-    for (int s = 0; s < per; s += 64) {
-        const int key = sort_key(ids, r0 + s + lane, R, E);
-        const uint64_t peers = peers_of(key, nbits);
-        if (key >= 0 && (peers & ((1ull << lane) - 1ull)) == 0)
-            wcount[wave][key] = (uint16_t)(wcount[wave][key] + __popcll(peers));
+    const uint64_t below = (1ull << lane) - 1ull;
+    auto count = [&](int key, uint64_t peers) {
+        if (key >= 0 && (peers & below) == 0) wcount[wave][key] = (uint16_t)(wcount[wave][key] + __popcll(peers));
         asm volatile("" ::: "memory");  // the next step reads what other lanes wrote (LDS keeps a wave's order)
+    };
+    int keys[KEEP ? KEEP : 1];
+    uint64_t peers_at[KEEP ? KEEP : 1];
+    if (KEEP) {
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u) keys[u] = 64 * u < per ? sort_key(ids, r0 + 64 * u + lane, R, E) : -1;
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u) {
+            peers_at[u] = 0;
+            if (64 * u >= per) continue;
+            peers_at[u] = peers_of(keys[u], nbits);
+            count(keys[u], peers_at[u]);
+        }
+    } else {
+        for (int s = 0; s < per; s += 64) {
+            const int key = sort_key(ids, r0 + s + lane, R, E);
+            count(key, peers_of(key, nbits));
+        }
     }
     // routes per expert of all chunks and of the chunks before this one
     if (counts) {
@@ -114,11 +133,13 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__
     __syncthreads();
     // exclusive prefix over the waves; the chunk's counts are the totals when it is the only one
     for (int e = tid; e <= E; e += 1024) {
-        int run = 0;
+        int run = 0, v[kSortWaves];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) v[w] = wcount[w][e];
+#pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const int v = wcount[w][e];
             wcount[w][e] = (uint16_t)run;
-            run += v;
+            run += v[w];
         }
         if (!counts) total[e] = run;
     }
@@ -143,11 +164,9 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__
         if (blk == 0) offsets[E] = kept;
     }
     __syncthreads();
-    for (int s = 0; s < per; s += 64) {
+    auto place = [&](int s, int key, uint64_t peers) {
         const long long r = r0 + s + lane;
-        const int key = sort_key(ids, r, R, E);
-        const uint64_t peers = peers_of(key, nbits);
-        const int rank = __popcll(peers & ((1ull << lane) - 1ull));
+        const int rank = __popcll(peers & below);
         int prior = 0;
         if (key >= 0) prior = wcount[wave][key];
         asm volatile("" ::: "memory");
@@ -157,6 +176,16 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__
             const int row = base[key] + prior + rank;
             row_to_route[row] = key < E ? (int)r : -1;
             route_to_row[r] = key < E ? row : -1;
+        }
+    };
+    if (KEEP) {
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u)
+            if (64 * u < per) place(64 * u, keys[u], peers_at[u]);
+    } else {
+        for (int s = 0; s < per; s += 64) {
+            const int key = sort_key(ids, r0 + s + lane, R, E);
+            place(s, key, peers_of(key, nbits));
         }
     }
 }
@@ -172,17 +201,17 @@ static int sort_chunk(long long R) {
 template <typename ID>
 static hipError_t launch_sort(const ID* ids, int R, int E, uint32_t* counts, int32_t* row_to_route,
                               int32_t* route_to_row, int32_t* offsets, hipStream_t s) {
-    if (R <= kSortOneBlock) {
-        const int chunk = (R + kSortMinChunk - 1) / kSortMinChunk * kSortMinChunk;
-        hipLaunchKernelGGL(sort_place_kernel<ID>, dim3(1), dim3(1024), 0, s, ids, R, E, chunk,
-                           (const uint32_t*)nullptr, row_to_route, route_to_row, offsets);
-    } else {
-        const int chunk = sort_chunk(R);
-        const int nblk = (R + chunk - 1) / chunk;
-        hipLaunchKernelGGL(sort_count_kernel<ID>, dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk, counts);
-        hipLaunchKernelGGL(sort_place_kernel<ID>, dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk,
-                           (const uint32_t*)counts, row_to_route, route_to_row, offsets);
-    }
+    const bool one = R <= kSortOneBlock;
+    const int chunk = one ? (R + kSortMinChunk - 1) / kSortMinChunk * kSortMinChunk : sort_chunk(R);
+    const int nblk = one ? 1 : (R + chunk - 1) / chunk;
+    if (!one) hipLaunchKernelGGL(sort_count_kernel<ID>, dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk, counts);
+    const uint32_t* c = one ? nullptr : counts;
+    if (chunk <= kKeep * kSortMinChunk)
+        hipLaunchKernelGGL((sort_place_kernel<ID, kKeep>), dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk, c,
+                           row_to_route, route_to_row, offsets);
+    else
+        hipLaunchKernelGGL((sort_place_kernel<ID, 0>), dim3(nblk), dim3(1024), 0, s, ids, R, E, chunk, c,
+                           row_to_route, route_to_row, offsets);
     return hipGetLastError();
 }
 

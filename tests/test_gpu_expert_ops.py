@@ -43,7 +43,7 @@ def say(*a):
 # ---------------------------------------------------------------------------
 SORTS = [(0, 2, 4), (1, 1, 1), (1, 8, 256), (3, 5, 2), (64, 8, 256), (63, 1, 64), (65, 1, 65), (513, 8, 7),
          (512, 8, 256), (513, 8, 256), (1024, 4, 1), (4097, 1, 300), (2048, 8, 1024), (5000, 3, 1024),
-         (16384, 8, 256), (40000, 8, 1023), (100000, 5, 33)]
+         (16384, 8, 256), (40000, 8, 1023), (100000, 5, 33), (70000, 16, 5), (300000, 8, 200)]
 
 
 @pytest.mark.parametrize("T,K,E", SORTS)
@@ -149,6 +149,42 @@ def test_dispatch_and_combine(T, K, H, E, dtype, pad):
             assert_within(dw2, want.reshape(T, K), bound, "dispatch_grad weights")
 
 
+@pytest.mark.parametrize("dtype", DT, ids=NAME.get)
+@pytest.mark.parametrize("T,K,H,E", [(4200, 4, 1032, 9), (2100, 8, 2056, 20), (2100, 10, 2056, 20), (5000, 3, 1544, 6)])
+def test_large_rows(T, K, H, E, dtype):
+    """Outputs of 32 MB and more (stored past the caches), rows of a wave and of a block
+    per token, against 64 bits on the GPU; some routes dropped."""
+    say("large rows", T, K, H, E, NAME[dtype])
+    g = torch.Generator(device=DEV).manual_seed(K)
+    ids = torch.randint(0, E + 2, (T, K), device=DEV, generator=g)
+    o = moe.sort_routes(ids, E)
+    kept = int(o.offsets[-1])
+    tok, rows = (torch.randn(n, H, device=DEV, generator=g).to(dtype) for n in (T, T * K))
+    rows[kept:] = float("nan")
+    w = torch.randn(T, K, device=DEV, generator=g)
+    route = o.row_to_route[:kept].long()
+    token, wr = route // K, w.double().view(-1)[route][:, None]
+    out = torch.full((T * K, H), 7.0, dtype=dtype, device=DEV)
+    moe.dispatch(tok, o, out=out)
+    assert torch.equal(out[:kept], tok[token]) and (out[kept:] == 7).all()
+    want = tok.double()[token] * wr
+    def within(got, want, mag, n):
+        b = n * U32 * mag
+        return bool(((got.double() - want).abs() <= b + (want.abs() + b) * HALF[dtype] + ref.TINY[dtype]).all())
+    drows, dw = moe.combine_grad(tok, o, rows, w, out=out)
+    assert within(drows[:kept], want, want.abs(), 1) and (out[kept:] == 7).all()
+    prod = rows[:kept].double() * tok.double()[token]
+    dots, dmag = (torch.zeros(T * K, dtype=torch.float64, device=DEV) for _ in range(2))
+    dots[route], dmag[route] = prod.sum(1), prod.abs().sum(1)
+    bound = (H + 1) * U32 * dmag.view(T, K)
+    assert bool(((dw.double() - dots.view(T, K)).abs() <= bound).all())
+    term = rows[:kept].double() * wr
+    y, mag = (torch.zeros(T, H, dtype=torch.float64, device=DEV).index_add_(0, token, v) for v in (term, term.abs()))
+    assert within(moe.combine(rows, o, w), y, mag, K + 1)
+    dx, dw = moe.dispatch_grad(rows, o, tok, w)
+    assert within(dx, y, mag, K + 1) and bool(((dw.double() - dots.view(T, K)).abs() <= bound).all())
+
+
 def test_rows_without_tokens():
     o = moe.sort_routes(torch.empty(0, 4, dtype=torch.int32, device=DEV), 8)
     x = torch.empty(0, 16, device=DEV)
@@ -244,7 +280,8 @@ def test_damaged_map_stays_in_range():
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", DT, ids=NAME.get)
 @pytest.mark.parametrize("M,N", [(1, 1), (3, 7), (2, 64), (5, 129), (70, 512), (33, 2048), (9, 2056), (4, 7168),
-                                 (3, 8200), (2, 20001), (1, 70000)])
+                                 (3, 8200), (2, 20001), (1, 70000),
+                                 (4100, 1023), (4097, 2000), (4096, 513)])
 def test_quantize_int8(M, N, dtype):
     say("quantize", M, N, NAME[dtype])
     g = rng(M * 7 + N)
