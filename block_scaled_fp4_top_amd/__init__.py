@@ -121,7 +121,7 @@ def _need(t, name, dtype, shape=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -381,27 +381,22 @@ def _float_type(t, name):
     return code
 
 
-@dataclass(frozen=True)
 class RouteOrder:
     """The routes r = t*K + k of T tokens sorted by expert (see sort_routes), int32:
     row_to_route [T*K], route_to_row [T*K], offsets [E+1]."""
-    row_to_route: torch.Tensor
-    route_to_row: torch.Tensor
-    offsets: torch.Tensor
-    T: int
-    K: int
-    E: int
+    __slots__ = ("row_to_route", "route_to_row", "offsets", "T", "K", "E")
 
-    def __post_init__(self):
-        R, dev = self.T * self.K, self.offsets.device
-        for name, n in (("row_to_route", R), ("route_to_row", R), ("offsets", self.E + 1)):
-            _need(getattr(self, name), name, torch.int32, (n,), dev)
+    def __init__(self, row_to_route: torch.Tensor, route_to_row: torch.Tensor, offsets: torch.Tensor,
+                 T: int, K: int, E: int):
+        _need(offsets, "offsets", torch.int32, (E + 1,))
+        _need(row_to_route, "row_to_route", torch.int32, (T * K,), offsets.device)
+        _need(route_to_row, "route_to_row", torch.int32, (T * K,), offsets.device)
+        self._set(row_to_route, route_to_row, offsets, T, K, E)
 
-    @classmethod
-    def _of(cls, *fields):  # of tensors made here: no checks
-        o = object.__new__(cls)
-        o.__dict__.update(zip(("row_to_route", "route_to_row", "offsets", "T", "K", "E"), fields))
-        return o
+    def _set(self, row_to_route, route_to_row, offsets, T, K, E):
+        self.row_to_route, self.route_to_row, self.offsets = row_to_route, route_to_row, offsets
+        self.T, self.K, self.E = T, K, E
+        return self
 
     def tensors(self):
         return self.row_to_route, self.route_to_row, self.offsets
@@ -446,7 +441,7 @@ def sort_routes(ids: torch.Tensor, E: int) -> RouteOrder:
     _check(_lib.moe_sort_routes(ids.data_ptr(), int(ids.dtype == torch.int64), T, K, E, p, n, p + n,
                                 p + n + 4 * R, p + n + 8 * R, _raw_stream(ids)))
     _, row_to_route, route_to_row, offsets = whole.split_with_sizes((ws, R, R, E + 1))
-    return RouteOrder._of(row_to_route, route_to_row, offsets, T, K, E)
+    return RouteOrder.__new__(RouteOrder)._set(row_to_route, route_to_row, offsets, T, K, E)
 
 
 @_on_stream

@@ -163,7 +163,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
     constexpr int BK = 128, SL = BK / 64;               // bytes of depth per step, slices per step
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // 1 KB loads of A and of B per wave and step
-    constexpr int L = LA + LB, BUF = (BM + BN) * BK;
+    constexpr int BUF = (BM + BN) * BK;
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && MT >= 1 && BM <= NW * 64 && BN <= NW * 64, "tile shape");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S * BUF];
     __shared__ int s_first[kMaxE];   // grouped: tiles of the lower experts
@@ -270,24 +270,28 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
         for (int i = 0; i < LB; ++i)
             boff[i] = (uint32_t)min((wave + NW * i) * 8 + lr, t.cols - 1) * (uint32_t)p.ldb + chunk_b(i);
     };
-    auto issue = [&](int kt, int buf) {
+    // loads of A that bring rows of the tile (or its first row's repeats up to the
+    // groups that are multiplied)
+    auto loads_of_a = [](int rows) { return rows > BM / 2 ? LA : rows > BM / 4 ? (LA + 1) / 2 : (LA + 3) / 4; };
+    auto issue = [&](int kt, int buf, int la) {
         const int k = kt * BK;
         // the last step of a depth that is no multiple of 128: chunks behind the row's
         // end take an offset that the buffer's range check answers with zeros
         const int left = p.Kd - k;
 #pragma unroll
         for (int i = 0; i < LA; ++i)
-            buffer_load_lds16(abase, a_bytes, left < BK && chunk_a(i) >= left ? kOutOfRange : aoff[i] + (uint32_t)k,
-                              lds + buf * BUF + (wave + NW * i) * 1024);
+            if (i < la) buffer_load_lds16(abase, a_bytes, left < BK && chunk_a(i) >= left ? kOutOfRange : aoff[i] + (uint32_t)k,
+                                          lds + buf * BUF + (wave + NW * i) * 1024);
 #pragma unroll
         for (int i = 0; i < LB; ++i)
             buffer_load_lds16(bbase, b_bytes, left < BK && chunk_b(i) >= left ? kOutOfRange : boff[i] + (uint32_t)k,
                               lds + buf * BUF + BM * BK + (wave + NW * i) * 1024);
     };
-    auto issue_first = [&]() {
+    auto issue_first = [&](const Tile& t) {
+        const int la = loads_of_a(t.rows);
 #pragma unroll
         for (int u = 0; u < S; ++u)
-            if (u < KT) issue(u, u);
+            if (u < KT) issue(u, u, la);
     };
 
     if (id >= last) return;
@@ -311,7 +315,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     look_up(t, route_of_row(t), 0);
     __syncthreads();
     address(t, 0);
-    issue_first();
+    issue_first(t);
     wait_loads();
 
     // Operands of 16 rows x 64 bytes: lane l holds row l % 16, chunk 4 s + l / 16 of slice s.
@@ -324,6 +328,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
 
     auto tile = [&](auto me_tag, int next_route) {
         constexpr int ME = decltype(me_tag)::value;
+        constexpr int LE = ME == MT ? LA : ME == (MT + 1) / 2 ? (LA + 1) / 2 : (LA + 3) / 4;  // loads_of_a
         // A slice's rows of A come in H parts of HM groups, which bounds the operands held
         constexpr int HM = ME > 4 ? 4 : ME, H = ME / HM, UNITS = SL * H;
         i32x4 fa[2][HM], fb[2][NT];
@@ -358,13 +363,13 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
             for (int u = 0; u < UNITS; ++u) {
                 const int sl = u / H, h = u % H;
                 if (u + 1 == UNITS) {
-                    if (kt + S <= KT) wait_and_barrier<(S - 2) * L>();
+                    if (kt + S <= KT) wait_and_barrier<(S - 2) * (LE + LB)>();
                     else wait_and_barrier<0>();
                     if (kt + 1 < KT) {
                         fetch_b(next, 0);
                         fetch_a(next, 0, 0);
                     }
-                    if (kt + S < KT) issue(kt + S, buf);
+                    if (kt + S < KT) issue(kt + S, buf, LE);
                 } else if (h + 1 < H) {
                     fetch_a(buf, sl, h + 1);
                 } else {
@@ -390,7 +395,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
             look_up(nt, next_route, par ^ 1);
             wait_lds_and_barrier();
             address(nt, par ^ 1);
-            issue_first();
+            issue_first(nt);
         }
 
         // acc[j][i][c]: row (i*WM + wm)*16 + lane % 16, column CQ (lane / 16) + 4 j + c
@@ -514,6 +519,32 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
     for (int j = 0; j < NS; ++j)
         bp[j] = p.b + (int64_t)e * p.b_expert + (int64_t)min(n0 + j * 16 + r16, p.N - 1) * p.ldb + quad * 16;
 
+    // the result's fragment that this wave joins in the end: its scales are requested
+    // first, so that they are there by then
+    static_assert(MS * NS <= NW, "one fragment per wave");
+    const int f = wave, m = (f % MS) * 16 + r16, n = n0 + (f / MS) * 16 + 4 * quad, left = p.N - n;
+    bool mine = f < MS * NS && m < rows && left > 0;
+    float sa = 0.0f;
+    Few<float, 4> sb = {}, bias = {};
+    if (mine) {
+        int ar = row0 + m;
+        if (p.row_to_route) ar = p.row_to_route[ar] / p.topk;
+        mine = (uint32_t)ar < (uint32_t)p.a_rows;
+        const size_t ne = (size_t)e * p.N + n;
+        if (mine) sa = p.sa[ar];
+        if (left >= 4) {
+            sb = *reinterpret_cast<const Few<float, 4>*>(p.sb + ne);
+            if (p.bias) bias = *reinterpret_cast<const Few<float, 4>*>(p.bias + ne);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+                if (c < left) {
+                    sb.e[c] = p.sb[ne + c];
+                    if (p.bias) bias.e[c] = p.bias[ne + c];
+                }
+        }
+    }
+
     i32x4 fa[P][2][MS], fb[P][2][NS];
     i32x4 acc[NS][MS];
 #pragma unroll
@@ -558,32 +589,20 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
         for (int i = 0; i < MS; ++i) part[wave][j * MS + i][lane] = acc[j][i];
     __syncthreads();
     // part[w][j * MS + i][lane][c]: row i * 16 + lane % 16, column j * 16 + 4 (lane / 16) + c
-    T* const y = static_cast<T*>(p.y);
-    for (int f = wave; f < MS * NS; f += NW) {
-        i32x4 sum = part[0][f][lane];
+    if (!mine) return;
+    i32x4 sum = part[0][f][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) sum += part[w][f][lane];
-        const int m = (f % MS) * 16 + r16, n = n0 + (f / MS) * 16 + 4 * quad, left = p.N - n;
-        if (m >= rows || left <= 0) continue;
-        int ar = row0 + m;
-        if (p.row_to_route) ar = p.row_to_route[ar] / p.topk;
-        if ((uint32_t)ar >= (uint32_t)p.a_rows) continue;
-        const float sa = p.sa[ar];
-        const size_t ne = (size_t)e * p.N + n;
-        T* dst = y + (int64_t)(row0 + m) * p.ldy + n;
-        Few<T, 4> o;
-        if (left >= 4) {
-            const Few<float, 4> sb = *reinterpret_cast<const Few<float, 4>*>(p.sb + ne);
-            Few<float, 4> bias = {};
-            if (p.bias) bias = *reinterpret_cast<const Few<float, 4>*>(p.bias + ne);
+    for (int w = 1; w < NW; ++w) sum += part[w][f][lane];
+    T* dst = static_cast<T*>(p.y) + (int64_t)(row0 + m) * p.ldy + n;
+    Few<T, 4> o;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o.e[c] = from_f32<T>(__fmaf_rn((float)sum[c] * sa, sb.e[c], bias.e[c]));
-            *reinterpret_cast<Few<T, 4>*>(dst) = o;
-        } else {
+    for (int c = 0; c < 4; ++c) o.e[c] = from_f32<T>(__fmaf_rn((float)sum[c] * sa, sb.e[c], bias.e[c]));
+    if (left >= 4) {
+        *reinterpret_cast<Few<T, 4>*>(dst) = o;
+    } else {
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-                if (c < left) dst[c] = from_f32<T>(__fmaf_rn((float)sum[c] * sa, p.sb[ne + c], p.bias ? p.bias[ne + c] : 0.0f));
-        }
+        for (int c = 0; c < 3; ++c)
+            if (c < left) dst[c] = o.e[c];
     }
 }
 
