@@ -1,8 +1,6 @@
 // Products of 8-bit integer matrices with a scale for each token (row of A)
-// and each output channel (row of B), dense or expert by expert, and the
-// quantizer of their activations.
-//   quantize: s[m] = max_j |x[m,j]| / 127, c[m,j] = round(x[m,j] / s[m])
-//   product:  y[m,n] = sa[m] sb[n] sum_k a[m,k] b[n,k] (+ bias[n])
+// and each output channel (row of B), dense or expert by expert:
+//   y[m,n] = sa[m] sb[n] sum_k a[m,k] b[n,k] (+ bias[n])
 // The sums are exact 32-bit integers (|sum| <= 2^14 * 131056 < 2^31), the scales
 // are applied in fp32 and the result is rounded once to the output's type.
 #include <algorithm>
@@ -18,9 +16,6 @@ namespace moe {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// ---------------------------------------------------------------------------
-// products
-// ---------------------------------------------------------------------------
 struct Int8Args {
     const int8_t* a;
     int64_t lda;
@@ -39,6 +34,15 @@ struct Int8Args {
     void* y;
     int64_t ldy;
 };
+
+// Row of A of row r of the result, -1 if there is none.
+__device__ __forceinline__ int row_of_route(const Int8Args& p, int route) {
+    const int ar = p.row_to_route ? route / p.topk : route;
+    return route >= 0 && ar < p.a_rows ? ar : -1;
+}
+__device__ __forceinline__ int row_of_a(const Int8Args& p, int r) {
+    return row_of_route(p, p.row_to_route ? p.row_to_route[r] : r);
+}
 
 // Rows of expert e. Offsets are clamped to [0, M], so a damaged list stays in range.
 __device__ __forceinline__ void expert_rows(const Int8Args& p, int e, int* lo, int* hi) {
@@ -98,8 +102,6 @@ __device__ __forceinline__ bool find_tile(const Int8Args& p, int tile, int lane,
 // ---------------------------------------------------------------------------
 // wide tiles
 // ---------------------------------------------------------------------------
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-
 template <typename T, int N>
 struct __attribute__((packed, aligned(sizeof(T)))) Few {
     T e[N];
@@ -158,6 +160,17 @@ constexpr uint32_t kOutOfRange = 0xFFFF0000u;
 //    loads of whole 128-byte lines.
 //  - The first S steps of the next tile are requested between a tile's last step
 //    and its epilogue.
+// 16384 x 4096 x 7168 in bf16 with 256 x 256 tiles: 427 us, 2.25 POP/s (the plain
+// library product of that size: 465 us, 2.07). It takes 340 us without the loads
+// and 366 without the products; neither the matrix cores (46 % busy) nor the LDS (no
+// bank conflicts) are full, the chip is at its power limit (1.7 - 1.95 GHz instead
+// of 2.4), which is why fewer bytes through the LDS and the L2 per product, and the
+// cheaper matrix instruction, are what made it faster: 32x32x32 products 516 us,
+// 16x16x64 450, results stored as whole lines past the caches 427. Half lines (64
+// bytes of depth per step, four or five buffers) and requests of lines ahead into
+// the L2 were slower (556, 490).
+// 128 groups of 32768 x 4096 x 4096 (mean 256 rows, up to 1300): 804 us; 662 without
+// the products: weights of 2.1 GB and rows re-read through the L2.
 template <typename T, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int ntiles) {
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
@@ -235,10 +248,6 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
         }
         return r;
     };
-    auto row_of_route = [&](int r) {
-        const int ar = p.row_to_route ? r / p.topk : r;
-        return r >= 0 && ar < p.a_rows ? ar : -1;
-    };
 
     // Staging: one load brings 8 rows of 128 bytes; lane l lands at byte 16 l of its
     // 1 KB, i.e. in slot l % 8 of row l / 8, and fetches chunk (l % 8) ^ mix(row). The
@@ -302,7 +311,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     // Row r < BM of a tile and column c < BN belong to thread r, c: row of A, scales, bias.
     auto look_up = [&](const Tile& t, int route, int par) {
         if (tid < BM) {
-            const int ar = row_of_route(route);
+            const int ar = row_of_route(p, route);
             s_arow[par][tid] = ar;
             my_sa = p.sa[max(ar, 0)];
         }
@@ -508,11 +517,7 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
     const int8_t *ap[MS], *bp[NS];
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
-        int ar = row0 + min(i * 16 + r16, rows - 1);
-        if (p.row_to_route) {
-            ar = p.row_to_route[ar] / p.topk;
-            ar = (uint32_t)ar < (uint32_t)p.a_rows ? ar : 0;
-        }
+        const int ar = max(row_of_a(p, row0 + min(i * 16 + r16, rows - 1)), 0);
         ap[i] = p.a + (int64_t)ar * p.lda + quad * 16;
     }
 #pragma unroll
@@ -527,9 +532,8 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
     float sa = 0.0f;
     Few<float, 4> sb = {}, bias = {};
     if (mine) {
-        int ar = row0 + m;
-        if (p.row_to_route) ar = p.row_to_route[ar] / p.topk;
-        mine = (uint32_t)ar < (uint32_t)p.a_rows;
+        const int ar = row_of_a(p, row0 + m);
+        mine = ar >= 0;
         const size_t ne = (size_t)e * p.N + n;
         if (mine) sa = p.sa[ar];
         if (left >= 4) {
@@ -615,9 +619,10 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 
 // The tile shape: the largest that still gives about one block per CU. A larger
 // tile moves fewer bytes per product, but a product that does not fill the CUs is
-// bound by the time of one block. Columns N = 4096, depth 7168, bf16, in us:
+// bound by the time of one block. Columns N = 4096, depth 7168, bf16, in us from
+// call to call (a call takes the host 9 to 10 us):
 //   rows      256x256  128x256  128x128  64x128  64x32  32x32  16x32  16x16
-//   16384         437      507
+//   16384         427      507
 //    2048          92       65       79
 //    1024          91       57       44      59
 //     512          91       56       40      32     92
@@ -625,7 +630,7 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 //     128          63       56       39      30     27     35
 //      64                             29      30     28     20     26
 //      32                             26             22     21     16     19
-//      16                             26             19     18     17     14
+//      16                             26             19     18     17     12
 // For experts the host knows the mean rows only: 64 tokens with 8 of 256 experts,
 // depth 7168: 758 us with 128x256 (6.0 TB/s of weights), 1044 or more with 16 rows;
 // 256-row tiles pay from about 192 mean rows on (128: 576 against 521 us, 1536: 482
@@ -658,7 +663,7 @@ static int run_int8_matmul(Int8Args p, int out_dtype, bool grouped, hipStream_t 
     if (p.Kd % 16) return reject(MOE_ERR_UNSUPPORTED, "the depth K=%d must be a multiple of 16", p.Kd);
     if (p.Kd >= 131072) return reject(MOE_ERR_UNSUPPORTED, "depth K=%d: 32-bit sums hold up to 131071 products", p.Kd);
     if (p.N > (1 << 20)) return reject(MOE_ERR_UNSUPPORTED, "N=%d above %d", p.N, 1 << 20);
-    if (p.M > (1 << 26)) return reject(MOE_ERR_UNSUPPORTED, "M=%d rows above %d", p.M, 1 << 26);
+    if (p.M > kMaxRows) return reject(MOE_ERR_UNSUPPORTED, "M=%d rows above %lld", p.M, (long long)kMaxRows);
     if (grouped && (p.E < 1 || p.E > kMaxE)) return reject(MOE_ERR_INVALID, "E=%d outside [1, %d]", p.E, kMaxE);
     if (p.row_to_route && (p.topk < 1 || p.topk > kMaxK))
         return reject(MOE_ERR_INVALID, "topk=%d outside [1, %d]", p.topk, kMaxK);
@@ -673,7 +678,7 @@ static int run_int8_matmul(Int8Args p, int out_dtype, bool grouped, hipStream_t 
     const int64_t far = (int64_t)1 << 23;  // 256 rows of a tile are addressed by 32-bit offsets
     if ((p.a_rows > 1 && p.lda > far) || (p.N > 1 && p.ldb > far) || (p.M > 1 && p.ldy > ((int64_t)1 << 31)))
         return reject(MOE_ERR_UNSUPPORTED, "a row stride above 2^23 bytes (a, b) or 2^31 elements (y)");
-    if (p.row_to_route && extent(p.a_rows, p.lda, p.Kd, 1) > kOutOfRange)
+    if (p.row_to_route && (int64_t)(p.a_rows - 1) * p.lda + p.Kd > (int64_t)kOutOfRange)
         return reject(MOE_ERR_UNSUPPORTED, "gathered rows of 4 GiB or more");
     const int64_t most = ((int64_t)(p.M + 15) / 16 + (grouped ? p.E : 0)) * ((p.N + 15) / 16);
     if (most >= ((int64_t)1 << 31)) return reject(MOE_ERR_UNSUPPORTED, "M=%d, N=%d: too many tiles", p.M, p.N);
@@ -684,15 +689,14 @@ static int run_int8_matmul(Int8Args p, int out_dtype, bool grouped, hipStream_t 
     if (!is_aligned(p.y, es) || !is_aligned(p.sa, 4) || !is_aligned(p.sb, 4) || !is_aligned(p.bias, 4) ||
         !is_aligned(p.offsets, 4) || !is_aligned(p.row_to_route, 4))
         return reject(MOE_ERR_INVALID, "misaligned pointer");
-    const size_t n_y = extent(p.M, p.ldy, p.N, (int)es);
-    const size_t E = grouped ? p.E : 1;
-    const struct { const void* p; size_t n; } in[] = {
-        {p.a, extent(p.a_rows, p.lda, p.Kd, 1)}, {p.sa, (size_t)p.a_rows * 4},
-        {p.b, (E - 1) * (size_t)p.b_expert + extent(p.N, p.ldb, p.Kd, 1)}, {p.sb, E * p.N * 4},
-        {p.bias, p.bias ? E * p.N * 4 : 0}, {p.offsets, grouped ? (E + 1) * 4 : 0},
-        {p.row_to_route, p.row_to_route ? (size_t)p.M * 4 : 0}};
-    for (const auto& b : in)
-        if (overlap(b.p, b.n, p.y, n_y)) return reject(MOE_ERR_INVALID, "the output overlaps an input");
+    const Bytes y = matrix(p.y, p.M, p.ldy, p.N, (int)es);
+    const int64_t E = grouped ? p.E : 1;
+    const Bytes in[] = {matrix(p.a, p.a_rows, p.lda, p.Kd, 1), flat(p.sa, (int64_t)p.a_rows * 4),
+                        // (all of the experts as one piece)
+                        flat(p.b, (E - 1) * p.b_expert + (int64_t)(p.N - 1) * p.ldb + p.Kd), flat(p.sb, E * p.N * 4),
+                        flat(p.bias, E * p.N * 4), flat(p.offsets, (E + 1) * 4), flat(p.row_to_route, (int64_t)p.M * 4)};
+    for (const Bytes& b : in)
+        if (overlap(b, y)) return reject(MOE_ERR_INVALID, "the output overlaps an input");
     hipError_t e;
     if (out_dtype == MOE_DT_BF16) e = launch_int8_matmul<Bf16>(p, stream);
     else if (out_dtype == MOE_DT_FP16) e = launch_int8_matmul<Fp16>(p, stream);

@@ -147,6 +147,7 @@ extern "C" int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, 
                                 int8_t* codes, int64_t codes_stride, float* scales, hipStream_t stream) {
     if (!dtype_ok(dtype)) return reject(MOE_ERR_INVALID, "dtype=%d is not a moe_dtype", dtype);
     if (rows < 0) return reject(MOE_ERR_INVALID, "rows=%d is negative", rows);
+    if (rows > kMaxRows) return reject(MOE_ERR_UNSUPPORTED, "rows=%d above %lld", rows, (long long)kMaxRows);
     if (cols < 1 || cols > (1 << 20)) return reject(MOE_ERR_UNSUPPORTED, "cols=%d outside [1, %d]", cols, 1 << 20);
     if (rows == 0) return MOE_OK;
     if (!x || !codes || !scales) return reject(MOE_ERR_INVALID, "NULL pointer argument");
@@ -155,9 +156,9 @@ extern "C" int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, 
         return reject(MOE_ERR_INVALID, "row strides %lld and %lld", (long long)x_stride, (long long)codes_stride);
     const size_t es = dtype_bytes(dtype);
     if (!is_aligned(x, es) || !is_aligned(scales, 4)) return reject(MOE_ERR_INVALID, "misaligned pointer");
-    const size_t nx = extent(rows, x_stride, cols, (int)es), nc = extent(rows, codes_stride, cols, 1), ns = (size_t)rows * 4;
-    if (overlap(x, nx, codes, nc) || overlap(x, nx, scales, ns) || overlap(codes, nc, scales, ns))
-        return reject(MOE_ERR_INVALID, "buffers overlap");
+    const Bytes bx = matrix(x, rows, x_stride, cols, (int)es), bc = matrix(codes, rows, codes_stride, cols, 1),
+                bs = flat(scales, (int64_t)rows * 4);
+    if (overlap(bx, bc) || overlap(bx, bs) || overlap(bc, bs)) return reject(MOE_ERR_INVALID, "buffers overlap");
     hipError_t e;
     if (dtype == MOE_DT_BF16) e = launch_int8_quantize((const Bf16*)x, x_stride, rows, cols, codes, codes_stride, scales, stream);
     else if (dtype == MOE_DT_FP16) e = launch_int8_quantize((const Fp16*)x, x_stride, rows, cols, codes, codes_stride, scales, stream);

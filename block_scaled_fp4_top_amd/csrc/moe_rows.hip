@@ -339,7 +339,7 @@ static int run_rows(bool spread, const char* what, int dtype, const RowArgs& a, 
     if (a.T < 0) return reject(MOE_ERR_INVALID, "T=%d is negative", a.T);
     if (a.K < 1 || a.K > kMaxK) return reject(MOE_ERR_INVALID, "K=%d outside [1, %d]", a.K, kMaxK);
     if (a.H < 1 || a.H > (1 << 20)) return reject(MOE_ERR_UNSUPPORTED, "H=%d outside [1, %d]", a.H, 1 << 20);
-    if (R > (1 << 26)) return reject(MOE_ERR_UNSUPPORTED, "T*K=%lld routes above %d", (long long)R, 1 << 26);
+    if (R > kMaxRows) return reject(MOE_ERR_UNSUPPORTED, "T*K=%lld routes above %lld", (long long)R, (long long)kMaxRows);
     if (a.dw && !a.w) return reject(MOE_ERR_INVALID, "a gradient of weights that are not there");
     if (a.T == 0) return MOE_OK;
     const bool tok = spread || a.dw, rows = !spread || a.dw;
@@ -357,15 +357,13 @@ static int run_rows(bool spread, const char* what, int dtype, const RowArgs& a, 
     if (!is_aligned(a.out, es) || (tok && !is_aligned(a.token_in, es)) || (rows && !is_aligned(a.rows_in, es)) ||
         !is_aligned(a.route_to_row, 4) || !is_aligned(a.w, 4) || !is_aligned(a.dw, 4))
         return reject(MOE_ERR_INVALID, "misaligned pointer");
-    const size_t n_out = extent(out_rows, a.ld_out, a.H, (int)es), n_dw = a.dw ? (size_t)R * 4 : 0;
-    const struct { const void* p; size_t n; } in[] = {
-        {tok ? a.token_in : nullptr, tok ? extent(a.T, a.ld_token_in, a.H, (int)es) : 0},
-        {rows ? a.rows_in : nullptr, rows ? extent(R, a.ld_rows_in, a.H, (int)es) : 0},
-        {a.route_to_row, (size_t)R * 4}, {a.w, a.w ? (size_t)R * 4 : 0}};
-    for (const auto& b : in)
-        if (overlap(b.p, b.n, a.out, n_out) || overlap(b.p, b.n, a.dw, n_dw))
-            return reject(MOE_ERR_INVALID, "an output overlaps an input");
-    if (overlap(a.out, n_out, a.dw, n_dw)) return reject(MOE_ERR_INVALID, "the outputs overlap");
+    const Bytes out = matrix(a.out, out_rows, a.ld_out, a.H, (int)es), dw = flat(a.dw, R * 4);
+    const Bytes in[] = {matrix(tok ? a.token_in : nullptr, a.T, a.ld_token_in, a.H, (int)es),
+                        matrix(rows ? a.rows_in : nullptr, R, a.ld_rows_in, a.H, (int)es),
+                        flat(a.route_to_row, R * 4), flat(a.w, R * 4)};
+    for (const Bytes& b : in)
+        if (overlap(b, out) || overlap(b, dw)) return reject(MOE_ERR_INVALID, "an output overlaps an input");
+    if (overlap(out, dw)) return reject(MOE_ERR_INVALID, "the outputs overlap");
     return launched(launch_rows(spread, dtype, a, stream), what);
 }
 

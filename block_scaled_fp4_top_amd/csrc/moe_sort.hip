@@ -10,6 +10,8 @@
 // and of this expert in earlier blocks) + routes of the expert in earlier waves
 // + in earlier steps of the wave + the rank. Left-out routes form a last group
 // with key E, which gives every entry of both maps a writer.
+#include <algorithm>
+
 #include "moe_args.h"
 #include "moe_route_dev.h"
 
@@ -18,7 +20,8 @@ namespace moe {
 constexpr int kSortWaves = 16;
 constexpr int kSortMinChunk = kSortWaves * 64;
 constexpr int kSortMaxChunk = 32768;         // per-wave counters are 16-bit
-constexpr long long kSortMaxR = 1LL << 26;
+constexpr int kSortBlocks = 256;              // at most (kMaxRows / kSortMaxChunk)
+static_assert(kMaxRows <= (int64_t)kSortBlocks * kSortMaxChunk, "every size has a chunk");
 constexpr long long kSortOneBlock = 4096;    // routes sorted by a single block
 
 __host__ __device__ inline int sort_row_words(int E) { return (E + 2) / 2; }  // E + 1 16-bit counts
@@ -191,10 +194,10 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(const ID* __restrict__
 }
 
 // Routes per block: the smallest power of two from kSortMinChunk that keeps the
-// blocks at 256 or fewer (each reads every block's counts), up to the largest.
+// blocks at kSortBlocks or fewer (each reads every block's counts).
 static int sort_chunk(long long R) {
     int c = kSortMinChunk;
-    while (c < kSortMaxChunk && (R + c - 1) / c > 256) c *= 2;
+    while (c < kSortMaxChunk && (R + c - 1) / c > kSortBlocks) c *= 2;
     return c;
 }
 
@@ -219,8 +222,8 @@ static int check_sort_sizes(int32_t T, int32_t K, int32_t E) {
     if (E < 1 || E > kMaxE) return reject(MOE_ERR_INVALID, "E=%d outside [1, %d]", E, kMaxE);
     if (T < 0) return reject(MOE_ERR_INVALID, "T=%d is negative", T);
     if (K < 1 || K > kMaxK) return reject(MOE_ERR_INVALID, "K=%d outside [1, %d]", K, kMaxK);
-    if ((long long)T * K > kSortMaxR)
-        return reject(MOE_ERR_UNSUPPORTED, "T*K=%lld routes above %lld", (long long)T * K, kSortMaxR);
+    if ((long long)T * K > (long long)kMaxRows)
+        return reject(MOE_ERR_UNSUPPORTED, "T*K=%lld routes above %lld", (long long)T * K, (long long)kMaxRows);
     return MOE_OK;
 }
 
@@ -231,9 +234,9 @@ using namespace moe;
 extern "C" size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t E) {
     if (check_sort_sizes(T, K, E) != MOE_OK) return 0;
     const long long R = (long long)T * K;
-    if (R <= kSortOneBlock) return 256;
-    const int chunk = sort_chunk(R);
-    return align256((size_t)((R + chunk - 1) / chunk) * sort_row_words(E) * 4);
+    // never less for fewer tokens: a workspace for T serves every smaller batch
+    const long long blocks = std::min((R + kSortMinChunk - 1) / kSortMinChunk, (long long)kSortBlocks);
+    return align256((size_t)std::max(blocks, 1LL) * sort_row_words(E) * 4);
 }
 
 extern "C" int moe_sort_routes(const void* ids, int32_t ids_are_wide, int32_t T, int32_t K, int32_t E,
@@ -251,12 +254,12 @@ extern "C" int moe_sort_routes(const void* ids, int32_t ids_are_wide, int32_t T,
     const size_t need = moe_sort_workspace_bytes(T, K, E);
     if (workspace_bytes < need)
         return reject(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
-    const struct { const void* p; size_t n; } b[] = {{ids, R * (ids_are_wide ? 8 : 4)}, {workspace, need},
-                                                    {row_to_route, R * 4}, {route_to_row, R * 4},
-                                                    {offsets, ((size_t)E + 1) * 4}};
+    const int64_t r4 = (int64_t)R * 4;
+    const Bytes b[] = {flat(ids, r4 * (ids_are_wide ? 2 : 1)), flat(workspace, (int64_t)need), flat(row_to_route, r4),
+                       flat(route_to_row, r4), flat(offsets, ((int64_t)E + 1) * 4)};
     for (int i = 0; i < 5; ++i)
         for (int j = i + 1; j < 5; ++j)
-            if (overlap(b[i].p, b[i].n, b[j].p, b[j].n)) return reject(MOE_ERR_INVALID, "buffers overlap");
+            if (overlap(b[i], b[j])) return reject(MOE_ERR_INVALID, "buffers overlap");
     uint32_t* counts = static_cast<uint32_t*>(workspace);
     return launched(ids_are_wide ? launch_sort(static_cast<const int64_t*>(ids), (int)R, E, counts, row_to_route,
                                                route_to_row, offsets, stream)

@@ -230,12 +230,14 @@ int moe_stage_times(float* ms, int32_t n, int32_t* forwards);
  *
  * Row strides are in elements; the elements of a row are contiguous. Pointers
  * are aligned to their element unless noted. Outputs must not share bytes with
- * inputs or with each other (MOE_ERR_INVALID). T = 0 (or no rows) is valid and
+ * inputs or with each other (MOE_ERR_INVALID; columns of one matrix that lie apart
+ * are fine). T = 0 (or no rows) is valid and
  * only writes what does not depend on rows. Nothing is kept between calls, so
  * calls on different streams are independent as long as their buffers are. */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 } moe_dtype;
 
-/* Workspace bytes of moe_sort_routes (0 if the sizes are invalid). */
+/* Workspace bytes of moe_sort_routes for up to T tokens (0 if the sizes are
+ * invalid). */
 size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t E);
 
 /* Stable sort of the routes by expert.
@@ -246,7 +248,7 @@ size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t E);
  *   offsets[e] .. offsets[e+1]-1 in ascending order; -1 in the rows from
  *   offsets[E] on.   route_to_row: [T*K] the row of each route, -1 if dropped.
  *   offsets: [E+1].   workspace: >= moe_sort_workspace_bytes(T, K, E) bytes,
- *   16-byte aligned.   1 <= E <= 1024, 1 <= K <= 64, T*K <= 2^26. */
+ *   16-byte aligned.   1 <= E <= 1024, 1 <= K <= 64, T*K <= 2^23. */
 int moe_sort_routes(const void* ids, int32_t ids_are_wide, int32_t T, int32_t K, int32_t E,
                     void* workspace, size_t workspace_bytes, int32_t* row_to_route,
                     int32_t* route_to_row, int32_t* offsets, hipStream_t stream);
@@ -255,7 +257,7 @@ int moe_sort_routes(const void* ids, int32_t ids_are_wide, int32_t T, int32_t K,
  *   x: [T][H], rows: [T*K][H], both of type `dtype` (moe_dtype). weights:
  *   [T][K] fp32, or NULL for 1 (the rows are then copies, bit for bit). Rows
  *   that no route names are left as they were. An entry of route_to_row outside
- *   [0, T*K) counts as dropped. 1 <= H <= 2^20, T*K <= 2^26. x_stride may be
+ *   [0, T*K) counts as dropped. 1 <= H <= 2^20, T*K <= 2^23. x_stride may be
  *   anything from 0 (one row for all tokens) on. */
 int moe_dispatch(const void* x, int64_t x_stride, int32_t dtype, const int32_t* route_to_row,
                  const float* weights, int32_t T, int32_t K, int32_t H, void* rows,
@@ -291,7 +293,8 @@ int moe_combine_grad(const void* dy, int64_t dy_stride, int32_t dtype, const int
  * even (the exact quotient of the fp32 scale, so the codes are reproducible bit
  * for bit), in [-127, 127]. A zero row has scale 0 and codes 0; a row with an
  * infinity or a NaN has that as its scale and codes 0 (products with it are NaN).
- *   x: [rows][cols] of type dtype, codes: [rows][cols].  1 <= cols <= 2^20. */
+ *   x: [rows][cols] of type dtype, codes: [rows][cols].  1 <= cols <= 2^20,
+ *   rows <= 2^23. */
 int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, int32_t rows, int32_t cols,
                      int8_t* codes, int64_t codes_stride, float* scales, hipStream_t stream);
 
@@ -300,7 +303,7 @@ int moe_int_quantize(const void* x, int64_t x_stride, int32_t dtype, int32_t row
  *   a: [M][K], b: [N][K] int8, 16-byte aligned with strides that are multiples
  *   of 16; bias: [N] fp32 or NULL; y: [M][N].  K a multiple of 16 below 131072
  *   (MOE_ERR_UNSUPPORTED otherwise, as for strides of a and b above 2^23, N above
- *   2^20 and M above 2^26). */
+ *   2^20 and M above 2^23). */
 int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, const int8_t* b,
                    int64_t b_stride, const float* b_scales, const float* bias, int32_t M, int32_t N,
                    int32_t K, int32_t out_dtype, void* y, int64_t y_stride, hipStream_t stream);

@@ -36,12 +36,23 @@ def test_sort_refuses():
 
 def test_sort_workspace_never_shrinks():
     last = 0
-    for T in (0, 1, 100, 2048, 2049, 5000, 100000, 1 << 20, 1 << 23):
+    for T in (0, 1, 100, 2048, 2049, 5000, 100000, 131072, 131073, 1 << 18, (1 << 18) + 1, 1 << 20, 1 << 22):
         n = L.moe_sort_workspace_bytes(T, 2, 64)
-        assert n > 0
-        if T <= 100000:
-            assert n >= last
-            last = n
+        assert n >= last and n > 0
+        last = n
+    assert L.moe_sort_workspace_bytes((1 << 22) + 1, 2, 64) == 0
+
+
+def test_columns_of_one_matrix_do_not_overlap():
+    """Buffers are compared row by row where their strides agree: only here the checks
+    after it are reached (K too large), else the call is refused as overlapping."""
+    def at(out, ld_out=128, H=64):
+        return L.moe_dispatch(A, 128, 2, B, C, 4, 1, H, out, ld_out, None), err()
+    # rows of 128 floats: x in columns 0..63; out in columns 32..95 overlaps
+    assert at(ctypes.c_void_p(A.value + 32 * 4)) == (1, "an output overlaps an input")
+    assert at(ctypes.c_void_p(A.value - 32 * 4)) == (1, "an output overlaps an input")
+    assert at(ctypes.c_void_p(A.value + 64 * 4), ld_out=127)[0] == 1  # other strides: refused
+    assert at(ctypes.c_void_p(A.value + 65 * 4))[0] == 1              # runs over into the next row's x
 
 
 def rows_call(name, src=A, ld=64, dt=0, r2=B, w=C, other=D, ldo=64, T=4, K=2, H=64, out=F, ld_out=64, dw=G):

@@ -185,6 +185,15 @@ def test_large_rows(T, K, H, E, dtype):
     assert within(dx, y, mag, K + 1) and bool(((dw.double() - dots.view(T, K)).abs() <= bound).all())
 
 
+def test_output_in_other_columns_of_the_input():
+    T, K, H, E = 6, 1, 40, 3
+    o, (r2r, rt2, off) = order_of(routes(2, T, K, E, False), E)
+    both = torch.randn(T, 2 * H, device=DEV)
+    x = both[:, :H].clone()
+    got = moe.dispatch(both[:, :H], o, out=both[:, H:])
+    assert torch.equal(got, x[torch.as_tensor(r2r, device=DEV).long()]) and torch.equal(both[:, :H], x)
+
+
 def test_rows_without_tokens():
     o = moe.sort_routes(torch.empty(0, 4, dtype=torch.int32, device=DEV), 8)
     x = torch.empty(0, 16, device=DEV)
@@ -273,6 +282,21 @@ def test_damaged_map_stays_in_range():
     out = torch.full((T * K, 8), -1.0, device=DEV)
     moe.int8_grouped_matmul(a, torch.ones(T, device=DEV), b, torch.ones(E, 8, device=DEV), bad, gather=True, out=out)
     assert (out[0] == -1).all() and (out[1:] == 16).all()
+
+
+@pytest.mark.parametrize("N", [8, 4000])  # narrow and wide tiles
+def test_routes_that_name_no_token(N):
+    T, K, E = 60, 2, 20
+    o, _ = order_of(routes(5, T, K, E, False), E)
+    r2r = o.row_to_route.clone()
+    r2r[3], r2r[50], r2r[-1] = -1, T * K, -(1 << 31)
+    bad = moe.RouteOrder(r2r, o.route_to_row, o.offsets, T, K, E)
+    a, b = torch.ones(T, 32, dtype=torch.int8, device=DEV), torch.ones(E, N, 32, dtype=torch.int8, device=DEV)
+    out = torch.full((T * K, N), -1.0, device=DEV)
+    moe.int8_grouped_matmul(a, torch.ones(T, device=DEV), b, torch.ones(E, N, device=DEV), bad, gather=True, out=out)
+    want = torch.full((T * K, N), 32.0, device=DEV)
+    want[[3, 50, T * K - 1]] = -1
+    assert torch.equal(out, want)
 
 
 # ---------------------------------------------------------------------------
