@@ -8,7 +8,6 @@ fallback: if the library is missing, importing the binding fails.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -317,51 +316,51 @@ def stage_times():
 # `stream` or that device's current stream; what they allocate belongs to that
 # stream. Matrices may have any row stride; the elements of a row are
 # contiguous. Gradients are functions of their own (autograd records nothing).
+# (Small calls are bound by the host, so what a call has made itself is not
+# checked again.)
 # ---------------------------------------------------------------------------
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on_stream(f):
-    """Runs f on the device of its first argument and on the stream it is given,
-    with both current, so that f itself only uses the current ones."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        first = args[0] if args else next(iter(kw.values()), None)
-        if not isinstance(first, torch.Tensor):
-            raise TypeError("the first argument must be a torch.Tensor")
-        if not first.is_cuda:
-            raise ValueError("the tensors must be on a GPU")
-        dev = first.device
-        if stream is None:
-            if dev.index == torch._C._cuda_getDevice():
-                return f(*args, **kw)
-            with torch.cuda.device(dev):
-                return f(*args, **kw)
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        with torch.cuda.stream(stream):
-            got = f(*args, **kw)
-            if not torch.cuda.is_current_stream_capturing():
-                for t in (*args, *kw.values()):  # may be freed while the stream still reads them
-                    for u in t.tensors() if isinstance(t, RouteOrder) else (t,):
-                        if isinstance(u, torch.Tensor):
-                            u.record_stream(stream)
-        return got
-    return call
+def _elsewhere(f, args, stream):
+    """f(*args) with the device of its first argument and `stream` current: for a call
+    on another device or stream than the current ones."""
+    first = args[0]
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("the first argument must be a torch.Tensor")
+    dev = first.device
+    if not first.is_cuda:
+        raise ValueError("the tensors must be on a GPU")
+    if stream is None:
+        with torch.cuda.device(dev):
+            return f(*args)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        got = f(*args)
+        if not torch.cuda.is_current_stream_capturing():
+            for t in args:  # may be freed while the stream still reads them
+                for u in t.tensors() if isinstance(t, RouteOrder) else (t,):
+                    if isinstance(u, torch.Tensor):
+                        u.record_stream(stream)
+    return got
 
 
-def _raw_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+def _device_index(t):
+    """The index of a tensor's GPU; -1 for anything else (which _elsewhere refuses)."""
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
-def _matrix(t, name, dtype, device, rows=None, cols=None):
-    """Checks a 2-D tensor with contiguous rows; returns its row stride."""
+def _matrix(t, name, dtype, index, rows=None, cols=None):
+    """Checks a 2-D tensor with contiguous rows on GPU `index`; returns its row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     shape = t.shape
     if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected "
@@ -370,6 +369,15 @@ def _matrix(t, name, dtype, device, rows=None, cols=None):
     if inner != 1 and shape[1] != 1:
         raise ValueError(f"the elements of a row of {name} must be contiguous")
     return ld
+
+
+def _vector(t, name, index, shape):
+    """Checks a contiguous fp32 tensor of this shape; returns its address."""
+    if t.__class__ is torch.Tensor and t.dtype is torch.float32 and t.get_device() == index and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, torch.float32, shape, torch.device("cuda", index))
+    return t.data_ptr()
 
 
 def _float_type(t, name):
@@ -384,7 +392,7 @@ def _float_type(t, name):
 class RouteOrder:
     """The routes r = t*K + k of T tokens sorted by expert (see sort_routes), int32:
     row_to_route [T*K], route_to_row [T*K], offsets [E+1]."""
-    __slots__ = ("row_to_route", "route_to_row", "offsets", "T", "K", "E")
+    __slots__ = ("row_to_route", "route_to_row", "offsets", "T", "K", "E", "index")
 
     def __init__(self, row_to_route: torch.Tensor, route_to_row: torch.Tensor, offsets: torch.Tensor,
                  T: int, K: int, E: int):
@@ -396,39 +404,37 @@ class RouteOrder:
     def _set(self, row_to_route, route_to_row, offsets, T, K, E):
         self.row_to_route, self.route_to_row, self.offsets = row_to_route, route_to_row, offsets
         self.T, self.K, self.E = T, K, E
+        self.index = offsets.get_device()
         return self
 
     def tensors(self):
         return self.row_to_route, self.route_to_row, self.offsets
 
 
-def _order(order, device, T=None):
+def _order(order, index, T=None):
     if not isinstance(order, RouteOrder):
         raise TypeError("order must be a RouteOrder (see sort_routes)")
-    if order.offsets.device != device:
-        raise ValueError(f"order is on {order.offsets.device}, expected {device}")
+    if order.index != index:
+        raise ValueError(f"order is on cuda:{order.index}, expected cuda:{index}")
     if T is not None and order.T != T:
         raise ValueError(f"order is of {order.T} tokens, expected {T}")
 
 
-def _weights(w, order, device):
-    if w is not None:
-        _need(w, "weights", torch.float32, (order.T, order.K), device)
-        return w.data_ptr()
-    return None
-
-
-@_on_stream
-def sort_routes(ids: torch.Tensor, E: int) -> RouteOrder:
+def sort_routes(ids: torch.Tensor, E: int, stream=None) -> RouteOrder:
     """Stable sort of the routes r = t*K + k by expert. ids: [T, K] int32 or int64
     expert ids; an id outside [0, E) drops its route. Rows offsets[e] ..
     offsets[e+1]-1 hold the routes of expert e in ascending order; row_to_route is
     -1 behind the last row, route_to_row -1 for a dropped route."""
-    if ids.dtype not in (torch.int32, torch.int64):
+    dev = _device_index(ids)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(sort_routes, (ids, E), stream)
+    wide = ids.dtype == torch.int64
+    if not wide and ids.dtype != torch.int32:
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
     if ids.dim() != 2:
         raise ValueError(f"ids must be [T, K], got {tuple(ids.shape)}")
-    _need(ids, "ids", ids.dtype)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
     T, K = ids.shape
     n = _lib.moe_sort_workspace_bytes(T, K, E)
     if n == 0:
@@ -438,184 +444,197 @@ def sort_routes(ids: torch.Tensor, E: int) -> RouteOrder:
     ws = n // 4
     whole = torch.empty(ws + 2 * R + E + 1, dtype=torch.int32, device=ids.device)
     p = whole.data_ptr()
-    _check(_lib.moe_sort_routes(ids.data_ptr(), int(ids.dtype == torch.int64), T, K, E, p, n, p + n,
-                                p + n + 4 * R, p + n + 8 * R, _raw_stream(ids)))
+    _check(_lib.moe_sort_routes(ids.data_ptr(), wide, T, K, E, p, n, p + n, p + n + 4 * R, p + n + 8 * R,
+                                _raw_stream(dev)))
     _, row_to_route, route_to_row, offsets = whole.split_with_sizes((ws, R, R, E + 1))
     return RouteOrder.__new__(RouteOrder)._set(row_to_route, route_to_row, offsets, T, K, E)
 
 
-@_on_stream
-def dispatch(x: torch.Tensor, order: RouteOrder, weights=None, out=None) -> torch.Tensor:
+def dispatch(x: torch.Tensor, order: RouteOrder, weights=None, out=None, stream=None) -> torch.Tensor:
     """Rows of the experts from token rows x [T, H]: out[row(t,k)] = weights[t,k] * x[t]
     (weights [T, K] fp32, or None for copies). out is [T*K, H]; its rows from
     offsets[E] on are left as they were (uninitialised if out is allocated here)."""
+    dev = _device_index(x)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(dispatch, (x, order, weights, out), stream)
     dt = _float_type(x, "x")
-    ld = _matrix(x, "x", x.dtype, x.device)
+    ld = _matrix(x, "x", x.dtype, dev)
     T, H = x.shape
-    _order(order, x.device, T)
-    w = _weights(weights, order, x.device)
+    _order(order, dev, T)
+    K = order.K
+    w = None if weights is None else _vector(weights, "weights", dev, (T, K))
     if out is None:
-        out = torch.empty((T * order.K, H), dtype=x.dtype, device=x.device)
-    ld_out = _matrix(out, "out", x.dtype, x.device, T * order.K, H)
-    _check(_lib.moe_dispatch(x.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w, T, order.K, H,
-                             out.data_ptr(), ld_out, _raw_stream(x)))
+        out, ld_out = torch.empty((T * K, H), dtype=x.dtype, device=x.device), H
+    else:
+        ld_out = _matrix(out, "out", x.dtype, dev, T * K, H)
+    _check(_lib.moe_dispatch(x.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w, T, K, H,
+                             out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
-@_on_stream
-def dispatch_grad(drows: torch.Tensor, order: RouteOrder, x=None, weights=None, out=None):
+def dispatch_grad(drows: torch.Tensor, order: RouteOrder, x=None, weights=None, out=None, stream=None):
     """Gradients of dispatch: (dx [T, H], dweights [T, K] fp32 or None). dweights needs
     weights and x (the dispatched tokens); with weights alone only dx is computed."""
+    dev = _device_index(drows)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(dispatch_grad, (drows, order, x, weights, out), stream)
     dt = _float_type(drows, "drows")
-    ld = _matrix(drows, "drows", drows.dtype, drows.device)
-    dev, H = drows.device, drows.shape[1]
     _order(order, dev)
     T, K = order.T, order.K
-    if drows.shape[0] != T * K:
-        raise ValueError(f"drows has {drows.shape[0]} rows, expected T*K = {T * K}")
-    w = _weights(weights, order, dev)
-    if x is not None and weights is None:
-        raise ValueError("x is only used for the gradient of weights, which are missing")
-    ldx = _matrix(x, "x", drows.dtype, dev, T, H) if x is not None else 0
-    dw = torch.empty((T, K), dtype=torch.float32, device=dev) if x is not None else None
+    ld = _matrix(drows, "drows", drows.dtype, dev, T * K)
+    H = drows.shape[1]
+    w = None if weights is None else _vector(weights, "weights", dev, (T, K))
+    xp, ldx, dw, dwp = None, 0, None, None
+    if x is not None:
+        if weights is None:
+            raise ValueError("x is only used for the gradient of weights, which are missing")
+        ldx, xp = _matrix(x, "x", drows.dtype, dev, T, H), x.data_ptr()
+        dw = torch.empty((T, K), dtype=torch.float32, device=drows.device)
+        dwp = dw.data_ptr()
     if out is None:
-        out = torch.empty((T, H), dtype=drows.dtype, device=dev)
-    ld_out = _matrix(out, "out", drows.dtype, dev, T, H)
-    _check(_lib.moe_dispatch_grad(drows.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w,
-                                  x.data_ptr() if x is not None else None, ldx, T, K, H, out.data_ptr(),
-                                  ld_out, dw.data_ptr() if dw is not None else None, _raw_stream(drows)))
+        out, ld_out = torch.empty((T, H), dtype=drows.dtype, device=drows.device), H
+    else:
+        ld_out = _matrix(out, "out", drows.dtype, dev, T, H)
+    _check(_lib.moe_dispatch_grad(drows.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w, xp, ldx, T, K, H,
+                                  out.data_ptr(), ld_out, dwp, _raw_stream(dev)))
     return out, dw
 
 
-@_on_stream
-def combine(rows: torch.Tensor, order: RouteOrder, weights=None, out=None) -> torch.Tensor:
+def combine(rows: torch.Tensor, order: RouteOrder, weights=None, out=None, stream=None) -> torch.Tensor:
     """Token rows from the experts' rows [T*K, H]: y[t] = sum_k weights[t,k] * rows[row(t,k)]
     over the routes that are kept (weights [T, K] fp32, or None for 1). fp32 sums in
     k order, one rounding to the type of rows. See also finalize."""
+    dev = _device_index(rows)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(combine, (rows, order, weights, out), stream)
     dt = _float_type(rows, "rows")
-    ld = _matrix(rows, "rows", rows.dtype, rows.device)
-    dev, H = rows.device, rows.shape[1]
     _order(order, dev)
     T, K = order.T, order.K
-    if rows.shape[0] != T * K:
-        raise ValueError(f"rows has {rows.shape[0]} rows, expected T*K = {T * K}")
-    w = _weights(weights, order, dev)
+    ld = _matrix(rows, "rows", rows.dtype, dev, T * K)
+    H = rows.shape[1]
+    w = None if weights is None else _vector(weights, "weights", dev, (T, K))
     if out is None:
-        out = torch.empty((T, H), dtype=rows.dtype, device=dev)
-    ld_out = _matrix(out, "out", rows.dtype, dev, T, H)
+        out, ld_out = torch.empty((T, H), dtype=rows.dtype, device=rows.device), H
+    else:
+        ld_out = _matrix(out, "out", rows.dtype, dev, T, H)
     _check(_lib.moe_combine(rows.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w, T, K, H,
-                            out.data_ptr(), ld_out, _raw_stream(rows)))
+                            out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
-@_on_stream
-def combine_grad(dy: torch.Tensor, order: RouteOrder, rows=None, weights=None, out=None):
+def combine_grad(dy: torch.Tensor, order: RouteOrder, rows=None, weights=None, out=None, stream=None):
     """Gradients of combine: (drows [T*K, H], dweights [T, K] fp32 or None). drows'
     rows from offsets[E] on are left as they were. dweights needs weights and rows
     (the combined rows)."""
+    dev = _device_index(dy)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(combine_grad, (dy, order, rows, weights, out), stream)
     dt = _float_type(dy, "dy")
-    ld = _matrix(dy, "dy", dy.dtype, dy.device)
-    dev = dy.device
+    ld = _matrix(dy, "dy", dy.dtype, dev)
     T, H = dy.shape
     _order(order, dev, T)
     K = order.K
-    w = _weights(weights, order, dev)
-    if rows is not None and weights is None:
-        raise ValueError("rows is only used for the gradient of weights, which are missing")
-    ldr = _matrix(rows, "rows", dy.dtype, dev, T * K, H) if rows is not None else 0
-    dw = torch.empty((T, K), dtype=torch.float32, device=dev) if rows is not None else None
+    w = None if weights is None else _vector(weights, "weights", dev, (T, K))
+    rp, ldr, dw, dwp = None, 0, None, None
+    if rows is not None:
+        if weights is None:
+            raise ValueError("rows is only used for the gradient of weights, which are missing")
+        ldr, rp = _matrix(rows, "rows", dy.dtype, dev, T * K, H), rows.data_ptr()
+        dw = torch.empty((T, K), dtype=torch.float32, device=dy.device)
+        dwp = dw.data_ptr()
     if out is None:
-        out = torch.empty((T * K, H), dtype=dy.dtype, device=dev)
-    ld_out = _matrix(out, "out", dy.dtype, dev, T * K, H)
-    _check(_lib.moe_combine_grad(dy.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w,
-                                 rows.data_ptr() if rows is not None else None, ldr, T, K, H, out.data_ptr(),
-                                 ld_out, dw.data_ptr() if dw is not None else None, _raw_stream(dy)))
+        out, ld_out = torch.empty((T * K, H), dtype=dy.dtype, device=dy.device), H
+    else:
+        ld_out = _matrix(out, "out", dy.dtype, dev, T * K, H)
+    _check(_lib.moe_combine_grad(dy.data_ptr(), ld, dt, order.route_to_row.data_ptr(), w, rp, ldr, T, K, H,
+                                 out.data_ptr(), ld_out, dwp, _raw_stream(dev)))
     return out, dw
 
 
-@_on_stream
-def quantize_int8(x: torch.Tensor, out=None):
+def quantize_int8(x: torch.Tensor, out=None, stream=None):
     """Symmetric 8-bit quantization of each row of x [M, N]: (codes int8 [M, N], scales
     fp32 [M]) with scales = max|x| / 127 and codes = x / scale rounded to nearest, ties
     to even. A row with an infinity or a NaN has that as its scale and codes 0."""
+    dev = _device_index(x)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(quantize_int8, (x, out), stream)
     dt = _float_type(x, "x")
-    ld = _matrix(x, "x", x.dtype, x.device)
+    ld = _matrix(x, "x", x.dtype, dev)
     M, N = x.shape
     if out is None:
-        out = torch.empty((M, N), dtype=torch.int8, device=x.device)
-    ld_out = _matrix(out, "out", torch.int8, x.device, M, N)
+        out, ld_out = torch.empty((M, N), dtype=torch.int8, device=x.device), N
+    else:
+        ld_out = _matrix(out, "out", torch.int8, dev, M, N)
     scales = torch.empty(M, dtype=torch.float32, device=x.device)
     _check(_lib.moe_int_quantize(x.data_ptr(), ld, dt, M, N, out.data_ptr(), ld_out, scales.data_ptr(),
-                                 _raw_stream(x)))
+                                 _raw_stream(dev)))
     return out, scales
 
 
-def _int8_out(out, out_dtype, M, N, dev):
+def _int8_out(out, out_dtype, M, N, t, dev):
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
-    elif out_dtype is not None and isinstance(out, torch.Tensor) and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        dt = DTYPES.get(torch.bfloat16 if out_dtype is None else out_dtype)
+        if dt is None:
+            raise TypeError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
+        return torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=t.device), dt, N
     dt = _float_type(out, "out")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     return out, dt, _matrix(out, "out", out.dtype, dev, M, N)
 
 
-@_on_stream
 def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, bias=None,
-                out_dtype=None, out=None) -> torch.Tensor:
+                out_dtype=None, out=None, stream=None) -> torch.Tensor:
     """y = a_scale[:, None] * b_scale * (a @ b.T) + bias for int8 a [M, K] (see
     quantize_int8) and b [N, K], fp32 a_scale [M], b_scale [N] and bias [N] (or None):
     exact integer sums, fp32 scaling, one rounding to out_dtype (bfloat16 unless
     given). K and the row strides are multiples of 16."""
-    lda = _matrix(a, "a", torch.int8, a.device)
-    dev = a.device
+    dev = _device_index(a)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(int8_matmul, (a, a_scale, b, b_scale, bias, out_dtype, out), stream)
+    lda = _matrix(a, "a", torch.int8, dev)
     M, K = a.shape
     ldb = _matrix(b, "b", torch.int8, dev, None, K)
     N = b.shape[0]
-    _need(a_scale, "a_scale", torch.float32, (M,), dev)
-    _need(b_scale, "b_scale", torch.float32, (N,), dev)
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (N,), dev)
-    out, dt, ldy = _int8_out(out, out_dtype, M, N, dev)
-    _check(_lib.moe_int_matmul(a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb, b_scale.data_ptr(),
-                               bias.data_ptr() if bias is not None else None, M, N, K, dt, out.data_ptr(),
-                               ldy, _raw_stream(a)))
+    sa, sb = _vector(a_scale, "a_scale", dev, (M,)), _vector(b_scale, "b_scale", dev, (N,))
+    bp = None if bias is None else _vector(bias, "bias", dev, (N,))
+    out, dt, ldy = _int8_out(out, out_dtype, M, N, a, dev)
+    _check(_lib.moe_int_matmul(a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, bp, M, N, K, dt, out.data_ptr(),
+                               ldy, _raw_stream(dev)))
     return out
 
 
-@_on_stream
 def int8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
                         order: RouteOrder, gather: bool = False, bias=None, out_dtype=None,
-                        out=None) -> torch.Tensor:
+                        out=None, stream=None) -> torch.Tensor:
     """int8_matmul expert by expert over sorted routes: row r of the result [T*K, N], of
     expert e, is row r of a [T*K, K] times b[e] ([E, N, K] int8, b_scale and bias [E, N]).
     gather: a holds the tokens' rows [T, K] (a_scale [T]) and row r reads the one of its
     route. Rows from offsets[E] on are left as they were (uninitialised if out is
     allocated here)."""
-    lda = _matrix(a, "a", torch.int8, a.device)
-    dev = a.device
+    dev = _device_index(a)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(int8_grouped_matmul, (a, a_scale, b, b_scale, order, gather, bias, out_dtype, out), stream)
     _order(order, dev)
     M, E = order.T * order.K, order.E
-    a_rows, K = a.shape
-    if a_rows != (order.T if gather else M):
-        raise ValueError(f"a has {a_rows} rows, expected {order.T if gather else M}")
+    rows = order.T if gather else M
+    lda = _matrix(a, "a", torch.int8, dev, rows)
+    K = a.shape[1]
     if not isinstance(b, torch.Tensor) or b.dim() != 3 or b.shape[0] != E or b.shape[2] != K:
         raise ValueError(f"b must be a tensor [{E}, N, {K}]")
-    N = b.shape[1]
     if b.dtype != torch.int8:
         raise TypeError(f"b must be torch.int8, got {b.dtype}")
-    if b.device != dev:
-        raise ValueError(f"b is on {b.device}, expected {dev}")
+    if b.get_device() != dev:
+        raise ValueError(f"b is on {b.device}, expected cuda:{dev}")
+    N = b.shape[1]
     be, ldb, inner = b.stride()
     if inner != 1 and K != 1:
         raise ValueError("the elements of a row of b must be contiguous")
-    _need(a_scale, "a_scale", torch.float32, (a_rows,), dev)
-    _need(b_scale, "b_scale", torch.float32, (E, N), dev)
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (E, N), dev)
-    out, dt, ldy = _int8_out(out, out_dtype, M, N, dev)
-    _check(_lib.moe_int_grouped_matmul(a.data_ptr(), lda, a_scale.data_ptr(), a_rows, b.data_ptr(), ldb, be,
-                                       b_scale.data_ptr(), bias.data_ptr() if bias is not None else None,
+    sa, sb = _vector(a_scale, "a_scale", dev, (rows,)), _vector(b_scale, "b_scale", dev, (E, N))
+    bp = None if bias is None else _vector(bias, "bias", dev, (E, N))
+    out, dt, ldy = _int8_out(out, out_dtype, M, N, a, dev)
+    _check(_lib.moe_int_grouped_matmul(a.data_ptr(), lda, sa, rows, b.data_ptr(), ldb, be, sb, bp,
                                        order.offsets.data_ptr(),
                                        order.row_to_route.data_ptr() if gather else None, order.K, M, N, K, E,
-                                       dt, out.data_ptr(), ldy, _raw_stream(a)))
+                                       dt, out.data_ptr(), ldy, _raw_stream(dev)))
     return out
