@@ -185,6 +185,85 @@ def test_large_rows(T, K, H, E, dtype):
     assert within(dx, y, mag, K + 1) and bool(((dw.double() - dots.view(T, K)).abs() <= bound).all())
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements and 4 GiB in every matrix: the last rows arrive right."""
+    T, K, H, E = 36000, 8, 8192, 5
+    R = T * K
+    g = torch.Generator(device=DEV).manual_seed(1)
+    o = moe.sort_routes(torch.randint(0, E, (T, K), device=DEV, generator=g), E)
+    x = torch.randn(T, H, device=DEV, generator=g).to(torch.bfloat16)
+    rows = moe.dispatch(x, o)
+    token = o.row_to_route.long() // K
+    for at in (slice(0, 64), slice(R // 2, R // 2 + 64), slice(R - 64, R)):
+        assert torch.equal(rows[at], x[token[at]])
+    w = torch.rand(T, K, device=DEV, generator=g)
+    y = moe.combine(rows, o, w)
+    at = slice(T - 64, T)
+    want = x[at].double() * w[at].double().sum(1, keepdim=True)
+    mag = x[at].double().abs() * w[at].double().sum(1, keepdim=True)
+    assert bool(((y[at].double() - want).abs() <= (K + 1) * U32 * mag + (want.abs() + 1e-6 * mag) * HALF[x.dtype] + 1e-38).all())
+    c, s = moe.quantize_int8(rows)
+    want_c, want_s = ref.quantize(f64(rows[R - 8:]))
+    assert np.array_equal(c[R - 8:].cpu().numpy(), want_c) and np.array_equal(f64(s[R - 8:]), want_s)
+    del rows
+    b, sb = torch.randint(-127, 128, (48, H), dtype=torch.int8, device=DEV, generator=g), torch.rand(48, device=DEV, generator=g)
+    y = moe.int8_matmul(c[-280000:], s[-280000:], b, sb, out_dtype=torch.float32)
+    want, bound = ref.matmul(c[-16:].cpu().numpy(), f64(s[-16:]), b.cpu().numpy(), f64(sb))
+    assert_within(y[-16:], want, stored(bound, want, torch.float32), "far rows of a")
+    del y
+    b, sb = torch.randint(-127, 128, (H, 32), dtype=torch.int8, device=DEV, generator=g), torch.rand(H, device=DEV, generator=g)
+    a = c[:, :32].contiguous()
+    y = moe.int8_matmul(a, s, b, sb)
+    want, bound = ref.matmul(a[-16:].cpu().numpy(), f64(s[-16:]), b.cpu().numpy(), f64(sb))
+    assert_within(y[-16:], want, stored(bound, want, torch.bfloat16), "far rows of y")
+    with pytest.raises(moe.MoeError) as e:  # 560000 x 8192 gathered: 4.6 GB
+        big = torch.empty(560000, H, dtype=torch.int8, device=DEV)
+        oo = moe.sort_routes(torch.zeros(560000, 1, dtype=torch.int32, device=DEV), 1)
+        moe.int8_grouped_matmul(big, torch.ones(560000, device=DEV), b.new_zeros(1, 16, H), torch.ones(1, 16, device=DEV),
+                                oo, gather=True)
+    assert e.value.code == 2
+
+
+def test_most_routes():
+    """2^23 routes, a third of them on one expert, some dropped."""
+    ids = rng(1).integers(-1, 7, (1 << 20, 8))
+    ids[: 1 << 18] = 3
+    o = moe.sort_routes(dev(ids.astype(np.int32)), 6)
+    for got, want in zip(o.tensors(), ref.sort_routes(ids, 6)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=NAME.get)
+def test_columns_that_begin_anywhere(dtype):
+    """Matrices whose first element and whose rows are aligned to their element only."""
+    T, K, H, E = 33, 3, 600, 4
+    o, (r2r, rt2, off) = order_of(routes(6, T, K, E, False), E)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x = torch.randn(T, H + 5, device=DEV, generator=g).to(dtype)[:, 1:H + 1]
+    rows = torch.full((T * K, H + 3), 2.0, device=DEV, dtype=dtype)
+    moe.dispatch(x, o, out=rows[:, 3:])
+    want = x[torch.as_tensor(r2r // K, device=DEV)]
+    assert torch.equal(rows[:, 3:], want) and (rows[:, :3] == 2).all()
+    w = torch.rand(T, K, device=DEV, generator=g)
+    y, dw = moe.dispatch_grad(rows[:, 3:], o, x, w)
+    z, dw2 = moe.dispatch_grad(want.contiguous(), o, x.contiguous(), w)
+    assert torch.equal(y, z) and torch.equal(dw, dw2) and torch.equal(y, moe.combine(want.contiguous(), o, w))
+    out = torch.zeros(T, H + 7, dtype=torch.int8, device=DEV)
+    c, s = moe.quantize_int8(x, out=out[:, 7:])
+    c2, s2 = moe.quantize_int8(x.contiguous())
+    assert torch.equal(c, c2) and torch.equal(s, s2) and not out[:, :7].any()
+
+
+def test_one_matrix_for_all_experts():
+    T, K, E, N, D = 30, 2, 6, 72, 64
+    o, _ = order_of(routes(6, T, K, E, False), E)
+    g = rng(2)
+    a, b, sa, sb = dev(codes(g, T, D)), dev(codes(g, N, D)), dev(scale(g, T)), dev(scale(g, N))
+    y = moe.int8_grouped_matmul(a, sa, b.expand(E, N, D), sb.expand(E, N).contiguous(), o, gather=True)
+    z = moe.dispatch(moe.int8_matmul(a, sa, b, sb), o)
+    assert torch.equal(y, z)
+
+
 def test_output_in_other_columns_of_the_input():
     T, K, H, E = 6, 1, 40, 3
     o, (r2r, rt2, off) = order_of(routes(2, T, K, E, False), E)
