@@ -11,6 +11,10 @@
 #include "moe_rows_dev.h"
 #include "moe_route_dev.h"
 
+// for the kernels' lambdas: what one captures would go through scratch memory if it
+// were called
+#define INLINE __attribute__((always_inline))
+
 namespace moe {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -33,6 +37,7 @@ struct Int8Args {
     int topk;
     void* y;
     int64_t ldy;
+    int b_once;  // set by the launcher: (nearly) every row of B is read by one M-tile
 };
 
 // Row of A of row r of the result, -1 if there is none.
@@ -109,9 +114,11 @@ struct __attribute__((packed, aligned(sizeof(T)))) Few {
 
 // Direct buffer -> LDS load of 16 bytes per lane from `base` + `off` (zeros from
 // `bytes` on): lane l's bytes land at dst + 16 l (dst is uniform across the wave).
+// ONCE: a non-temporal load, for lines that are read once.
+template <bool ONCE>
 __device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t bytes, uint32_t off, void* dst) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000),
-                                             (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+                                             (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, ONCE ? 2 : 0);
 }
 
 // s_waitcnt until no vector-memory and no LDS operation of this wave is
@@ -211,7 +218,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     struct Tile {
         int e, row0, rows, n0, cols;
     };
-    auto locate = [&](int i) {
+    auto locate = [&](int i) INLINE {
         Tile t;
         int lo = 0, hi = p.M;
         t.e = 0;
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     };
     // Thread r < BM looks up row r of the tile: first the route, later the row of A
     // and its scale (rows behind the tile's last repeat its first).
-    auto route_of_row = [&](const Tile& t) {
+    auto route_of_row = [&](const Tile& t) INLINE {
         int r = 0;
         if (tid < BM) {
             r = t.row0 + (tid < t.rows ? tid : 0);
@@ -265,7 +272,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     const int KT = (p.Kd + BK - 1) / BK;
     const int8_t *abase, *bbase;
     uint32_t a_bytes, b_bytes, aoff[LA], boff[LB];
-    auto address = [&](const Tile& t, int par) {
+    auto address = [&](const Tile& t, int par) INLINE {
         abase = p.row_to_route ? p.a : p.a + (int64_t)t.row0 * p.lda;
         bbase = p.b + (int64_t)t.e * p.b_expert + (int64_t)t.n0 * p.ldb;
         a_bytes = (uint32_t)((int64_t)((p.row_to_route ? p.a_rows : t.rows) - 1) * p.lda + p.Kd);
@@ -282,21 +289,26 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     // loads of A that bring rows of the tile (or its first row's repeats up to the
     // groups that are multiplied)
     auto loads_of_a = [](int rows) { return rows > BM / 2 ? LA : rows > BM / 4 ? (LA + 1) / 2 : (LA + 3) / 4; };
-    auto issue = [&](int kt, int buf, int la) {
+    auto issue = [&](int kt, int buf, int la) INLINE {
         const int k = kt * BK;
         // the last step of a depth that is no multiple of 128: chunks behind the row's
         // end take an offset that the buffer's range check answers with zeros
         const int left = p.Kd - k;
 #pragma unroll
         for (int i = 0; i < LA; ++i)
-            if (i < la) buffer_load_lds16(abase, a_bytes, left < BK && chunk_a(i) >= left ? kOutOfRange : aoff[i] + (uint32_t)k,
+            if (i < la) buffer_load_lds16<false>(abase, a_bytes, left < BK && chunk_a(i) >= left ? kOutOfRange : aoff[i] + (uint32_t)k,
                                           lds + buf * BUF + (wave + NW * i) * 1024);
+        auto load_b = [&](auto once) INLINE {
 #pragma unroll
-        for (int i = 0; i < LB; ++i)
-            buffer_load_lds16(bbase, b_bytes, left < BK && chunk_b(i) >= left ? kOutOfRange : boff[i] + (uint32_t)k,
-                              lds + buf * BUF + BM * BK + (wave + NW * i) * 1024);
+            for (int i = 0; i < LB; ++i)
+                buffer_load_lds16<decltype(once)::value>(
+                    bbase, b_bytes, left < BK && chunk_b(i) >= left ? kOutOfRange : boff[i] + (uint32_t)k,
+                    lds + buf * BUF + BM * BK + (wave + NW * i) * 1024);
+        };
+        if (p.b_once) load_b(std::true_type{});
+        else load_b(std::false_type{});
     };
-    auto issue_first = [&](const Tile& t) {
+    auto issue_first = [&](const Tile& t) INLINE {
         const int la = loads_of_a(t.rows);
 #pragma unroll
         for (int u = 0; u < S; ++u)
@@ -309,7 +321,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     int par = 0;
     float my_sa = 0.0f, my_sb = 0.0f, my_bias = 0.0f;
     // Row r < BM of a tile and column c < BN belong to thread r, c: row of A, scales, bias.
-    auto look_up = [&](const Tile& t, int route, int par) {
+    auto look_up = [&](const Tile& t, int route, int par) INLINE {
         if (tid < BM) {
             const int ar = row_of_route(p, route);
             s_arow[par][tid] = ar;
@@ -335,18 +347,18 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     T* const y = static_cast<T*>(p.y);
     bool more;
 
-    auto tile = [&](auto me_tag, int next_route) {
+    auto tile = [&](auto me_tag, int next_route) INLINE {
         constexpr int ME = decltype(me_tag)::value;
         constexpr int LE = ME == MT ? LA : ME == (MT + 1) / 2 ? (LA + 1) / 2 : (LA + 3) / 4;  // loads_of_a
         // A slice's rows of A come in H parts of HM groups, which bounds the operands held
         constexpr int HM = ME > 4 ? 4 : ME, H = ME / HM, UNITS = SL * H;
         i32x4 fa[2][HM], fb[2][NT];
-        auto fetch_b = [&](int buf, int sl) {
+        auto fetch_b = [&](int buf, int sl) INLINE {
             const int o = buf * BUF + (slot_b ^ (sl << 6)) + b_at;
 #pragma unroll
             for (int j = 0; j < NT; ++j) fb[sl & 1][j] = *reinterpret_cast<const i32x4*>(&lds[o + j * 4 * BK]);
         };
-        auto fetch_a = [&](int buf, int sl, int h) {
+        auto fetch_a = [&](int buf, int sl, int h) INLINE {
             const int o = buf * BUF + (slot_a ^ (sl << 6)) + a_at;
 #pragma unroll
             for (int i = 0; i < HM; ++i)
@@ -555,7 +567,7 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
     for (int j = 0; j < NS; ++j)
 #pragma unroll
         for (int i = 0; i < MS; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
-    auto load = [&](int st, int k) {
+    auto load = [&](int st, int k) INLINE {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const bool in = k + s * 64 + quad * 16 < p.Kd;
@@ -567,7 +579,7 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
                 fa[st][s][i] = in ? *reinterpret_cast<const i32x4*>(ap[i] + k + s * 64) : i32x4{0, 0, 0, 0};
         }
     };
-    auto multiply = [&](int st) {
+    auto multiply = [&](int st) INLINE {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -637,13 +649,19 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 // against 528). A single token's broadcast rows cost the narrow tiles nothing:
 // 28672 x 8192 takes 49 us with 16x16 and 52 with 128x128; with 16 rows it is 71
 // and 53.
+// Where B is read about once, its loads are non-temporal: 64 x 8 routes over 256
+// experts of 4096 x 7168 800 -> 712 us, mean rows of 4, 16, 32, 48 over 128 experts
+// of 4096 x 4096 290 -> 260, 360 -> 325, 397 -> 371, 407 -> 391; of 64 rows 422 ->
+// 444. One matrix of 28672 x 8192 with 8, 64, 128, 200 rows 51 -> 47, 53 -> 49,
+// 61 -> 55, 80 -> 76.
 template <typename T>
-static hipError_t launch_int8_matmul(const Int8Args& p, hipStream_t s) {
+static hipError_t launch_int8_matmul(Int8Args p, hipStream_t s) {
     const int64_t groups = p.offsets ? std::min(p.E, p.M) : 1;
     const int64_t mean = (p.M + groups - 1) / groups;
     auto blocks = [&](int bm, int bn) { return groups * ((mean + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
     const int64_t cus = std::max(cu_count(), 8), full = cus * 7 / 8;
     const bool one = !p.offsets && p.M <= 4;
+    p.b_once = p.offsets ? mean <= 48 : p.M <= 256;
     if (!one && mean >= 192 && blocks(256, 256) >= full) launch_wide<T, 256, 256, 2, 4, 2>(p, s);
     else if (!one && blocks(128, 256) >= full) launch_wide<T, 128, 256, 2, 4, 3>(p, s);
     else if (!one && blocks(128, 128) >= full) launch_wide<T, 128, 128, 2, 4, 4>(p, s);
@@ -712,7 +730,7 @@ extern "C" int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_
                               int64_t b_stride, const float* b_scales, const float* bias, int32_t M, int32_t N,
                               int32_t K, int32_t out_dtype, void* y, int64_t y_stride, hipStream_t stream) {
     return run_int8_matmul(Int8Args{a, a_stride, a_scales, b, b_stride, 0, b_scales, bias, M, N, K, M, nullptr, 0,
-                                    nullptr, 1, y, y_stride},
+                                    nullptr, 1, y, y_stride, 0},
                            out_dtype, false, stream);
 }
 
@@ -725,6 +743,6 @@ extern "C" int moe_int_grouped_matmul(const int8_t* a, int64_t a_stride, const f
     if (a_rows < 0 || (!row_to_route && a_rows != M))
         return reject(MOE_ERR_INVALID, "a has %d rows, the output %d", a_rows, M);
     return run_int8_matmul(Int8Args{a, a_stride, a_scales, b, b_stride, b_expert_stride, b_scales, bias, M, N, K,
-                                    a_rows, offsets, E, row_to_route, topk, y, y_stride},
+                                    a_rows, offsets, E, row_to_route, topk, y, y_stride, 0},
                            out_dtype, true, stream);
 }
