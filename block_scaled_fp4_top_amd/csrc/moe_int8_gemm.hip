@@ -37,7 +37,6 @@ struct Int8Args {
     int topk;
     void* y;
     int64_t ldy;
-    int b_once;  // set by the launcher: (nearly) every row of B is read by one M-tile
 };
 
 // Row of A of row r of the result, -1 if there is none.
@@ -114,7 +113,11 @@ struct __attribute__((packed, aligned(sizeof(T)))) Few {
 
 // Direct buffer -> LDS load of 16 bytes per lane from `base` + `off` (zeros from
 // `bytes` on): lane l's bytes land at dst + 16 l (dst is uniform across the wave).
-// ONCE: a non-temporal load, for lines that are read once.
+// ONCE: a non-temporal load, for lines that are read once: the rows of B of an
+// expert with one M-tile. 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us;
+// mean rows of 16, 48, 64, 128 over 128 experts of 4096 x 4096 359 -> 325, 406 -> 377,
+// 422 -> 404, 516 -> 504 (with all of B non-temporal 326, 391, 443, 540: experts with
+// several tiles then lose their L2).
 template <bool ONCE>
 __device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t bytes, uint32_t off, void* dst) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000),
@@ -217,6 +220,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
 
     struct Tile {
         int e, row0, rows, n0, cols;
+        bool once;  // the only M-tile of its rows of B
     };
     auto locate = [&](int i) INLINE {
         Tile t;
@@ -238,6 +242,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
         const int group = i / (GM * ntiles), in = i - group * GM * ntiles;
         const int gm = min(GM, tiles - group * GM);
         const int nb = in / gm, mt = group * GM + in - nb * gm;
+        t.once = tiles == 1;
         t.n0 = nb * BN;
         t.cols = min(BN, p.N - t.n0);
         t.e = __builtin_amdgcn_readfirstlane(t.e);
@@ -272,9 +277,11 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
     const int KT = (p.Kd + BK - 1) / BK;
     const int8_t *abase, *bbase;
     uint32_t a_bytes, b_bytes, aoff[LA], boff[LB];
+    bool b_once;
     auto address = [&](const Tile& t, int par) INLINE {
         abase = p.row_to_route ? p.a : p.a + (int64_t)t.row0 * p.lda;
         bbase = p.b + (int64_t)t.e * p.b_expert + (int64_t)t.n0 * p.ldb;
+        b_once = t.once;
         a_bytes = (uint32_t)((int64_t)((p.row_to_route ? p.a_rows : t.rows) - 1) * p.lda + p.Kd);
         b_bytes = (uint32_t)((int64_t)(t.cols - 1) * p.ldb + p.Kd);
 #pragma unroll
@@ -305,7 +312,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
                     bbase, b_bytes, left < BK && chunk_b(i) >= left ? kOutOfRange : boff[i] + (uint32_t)k,
                     lds + buf * BUF + BM * BK + (wave + NW * i) * 1024);
         };
-        if (p.b_once) load_b(std::true_type{});
+        if (b_once) load_b(std::true_type{});
         else load_b(std::false_type{});
     };
     auto issue_first = [&](const Tile& t) INLINE {
@@ -649,19 +656,13 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 // against 528). A single token's broadcast rows cost the narrow tiles nothing:
 // 28672 x 8192 takes 49 us with 16x16 and 52 with 128x128; with 16 rows it is 71
 // and 53.
-// Where B is read about once, its loads are non-temporal: 64 x 8 routes over 256
-// experts of 4096 x 7168 800 -> 712 us, mean rows of 4, 16, 32, 48 over 128 experts
-// of 4096 x 4096 290 -> 260, 360 -> 325, 397 -> 371, 407 -> 391; of 64 rows 422 ->
-// 444. One matrix of 28672 x 8192 with 8, 64, 128, 200 rows 51 -> 47, 53 -> 49,
-// 61 -> 55, 80 -> 76.
 template <typename T>
-static hipError_t launch_int8_matmul(Int8Args p, hipStream_t s) {
+static hipError_t launch_int8_matmul(const Int8Args& p, hipStream_t s) {
     const int64_t groups = p.offsets ? std::min(p.E, p.M) : 1;
     const int64_t mean = (p.M + groups - 1) / groups;
     auto blocks = [&](int bm, int bn) { return groups * ((mean + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
     const int64_t cus = std::max(cu_count(), 8), full = cus * 7 / 8;
     const bool one = !p.offsets && p.M <= 4;
-    p.b_once = p.offsets ? mean <= 48 : p.M <= 256;
     if (!one && mean >= 192 && blocks(256, 256) >= full) launch_wide<T, 256, 256, 2, 4, 2>(p, s);
     else if (!one && blocks(128, 256) >= full) launch_wide<T, 128, 256, 2, 4, 3>(p, s);
     else if (!one && blocks(128, 128) >= full) launch_wide<T, 128, 128, 2, 4, 4>(p, s);
@@ -730,7 +731,7 @@ extern "C" int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_
                               int64_t b_stride, const float* b_scales, const float* bias, int32_t M, int32_t N,
                               int32_t K, int32_t out_dtype, void* y, int64_t y_stride, hipStream_t stream) {
     return run_int8_matmul(Int8Args{a, a_stride, a_scales, b, b_stride, 0, b_scales, bias, M, N, K, M, nullptr, 0,
-                                    nullptr, 1, y, y_stride, 0},
+                                    nullptr, 1, y, y_stride},
                            out_dtype, false, stream);
 }
 
@@ -743,6 +744,6 @@ extern "C" int moe_int_grouped_matmul(const int8_t* a, int64_t a_stride, const f
     if (a_rows < 0 || (!row_to_route && a_rows != M))
         return reject(MOE_ERR_INVALID, "a has %d rows, the output %d", a_rows, M);
     return run_int8_matmul(Int8Args{a, a_stride, a_scales, b, b_stride, b_expert_stride, b_scales, bias, M, N, K,
-                                    a_rows, offsets, E, row_to_route, topk, y, y_stride, 0},
+                                    a_rows, offsets, E, row_to_route, topk, y, y_stride},
                            out_dtype, true, stream);
 }
