@@ -653,9 +653,11 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 // For experts the host knows the mean rows only: 64 tokens with 8 of 256 experts,
 // depth 7168: 758 us with 128x256 (6.0 TB/s of weights), 1044 or more with 16 rows;
 // 256-row tiles pay from about 192 mean rows on (128: 576 against 521 us, 1536: 482
-// against 528). A single token's broadcast rows cost the narrow tiles nothing:
-// 28672 x 8192 takes 49 us with 16x16 and 52 with 128x128; with 16 rows it is 71
-// and 53.
+// against 528). Narrow tiles are no higher than the rows: 16 x 7168 x 7168 takes 18 us
+// with 16x32 and 19 with 64x32, 32 rows 21 with 32x32 and 23 with 64x32. A single
+// token's rows are broadcast, which favours 16x16 (1 x 14336 x 4096: 14.7 us, 64x128
+// 16.2; with 16 rows 20.6 and 17.2) until the wide tiles fill the CUs (1 x 28672 x
+// 8192: 46.9 and 45.9).
 template <typename T>
 static hipError_t launch_int8_matmul(const Int8Args& p, hipStream_t s) {
     const int64_t groups = p.offsets ? std::min(p.E, p.M) : 1;
@@ -663,12 +665,12 @@ static hipError_t launch_int8_matmul(const Int8Args& p, hipStream_t s) {
     auto blocks = [&](int bm, int bn) { return groups * ((mean + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
     const int64_t cus = std::max(cu_count(), 8), full = cus * 7 / 8;
     const bool one = !p.offsets && p.M <= 4;
-    if (!one && mean >= 192 && blocks(256, 256) >= full) launch_wide<T, 256, 256, 2, 4, 2>(p, s);
-    else if (!one && blocks(128, 256) >= full) launch_wide<T, 128, 256, 2, 4, 3>(p, s);
-    else if (!one && blocks(128, 128) >= full) launch_wide<T, 128, 128, 2, 4, 4>(p, s);
-    else if (!one && blocks(64, 128) >= cus * 3 / 8) launch_wide<T, 64, 128, 1, 8, 5>(p, s);
-    else if (!one && blocks(64, 32) >= full) launch_narrow<T, 4, 2, 8, 2>(p, s);
-    else if (!one && blocks(32, 32) >= full) launch_narrow<T, 2, 2, 8, 3>(p, s);
+    if (mean >= 192 && blocks(256, 256) >= full) launch_wide<T, 256, 256, 2, 4, 2>(p, s);
+    else if (blocks(128, 256) >= full) launch_wide<T, 128, 256, 2, 4, 3>(p, s);
+    else if (blocks(128, 128) >= full) launch_wide<T, 128, 128, 2, 4, 4>(p, s);
+    else if (blocks(64, 128) >= (one ? full : cus * 3 / 8)) launch_wide<T, 64, 128, 1, 8, 5>(p, s);
+    else if (mean > 32 && blocks(64, 32) >= full) launch_narrow<T, 4, 2, 8, 2>(p, s);
+    else if (mean > 16 && blocks(32, 32) >= full) launch_narrow<T, 2, 2, 8, 3>(p, s);
     else if (!one && blocks(16, 32) >= full) launch_narrow<T, 1, 2, 8, 3>(p, s);
     else launch_narrow<T, 1, 1, 8, 4>(p, s);
     return hipGetLastError();

@@ -450,7 +450,7 @@ MATMULS = [(1, 1, 16), (1, 17, 32), (1, 4096, 512), (2, 16, 48), (3, 300, 64), (
            (257, 513, 400), (300, 1024, 1024), (513, 777, 176), (1000, 520, 640), (1025, 1100, 336),
            # every tile shape on a chip of 256 CUs, with ragged edges: 16x32, 32x32, 64x32, 64x128, 128x128, 128x256
            # and 256x256, depths of one step, of several and with a cut last step
-           (16, 7200, 272), (30, 7190, 656), (60, 7201, 144), (300, 2601, 304), (301, 2602, 1296), (1000, 3603, 16),
+           (1, 28690, 80), (16, 7200, 272), (30, 7190, 656), (60, 7201, 144), (300, 2601, 304), (301, 2602, 1296), (1000, 3603, 16),
            (999, 3601, 400), (1801, 4002, 128), (1799, 4001, 272), (4000, 3702, 176), (3851, 3841, 256), (3999, 3701, 528)]
 
 
