@@ -170,16 +170,16 @@ constexpr uint32_t kOutOfRange = 0xFFFF0000u;
 //    loads of whole 128-byte lines.
 //  - The first S steps of the next tile are requested between a tile's last step
 //    and its epilogue.
-// 16384 x 4096 x 7168 in bf16 with 256 x 256 tiles: 404 us, 2.38 POP/s (the plain
+// 16384 x 4096 x 7168 in bf16 with 256 x 256 tiles: 408 us, 2.36 POP/s (the plain
 // library product of that size: 465 us, 2.07). Built up to whole-line stores it took
 // 340 us without its loads and 366 without its products; neither the matrix cores
 // (51 % busy) nor the LDS (no bank conflicts) are full, the chip is at its power limit
 // (1.7 - 1.95 GHz instead of 2.4), which is why fewer bytes through the LDS and the
 // L2 per product, and the cheaper matrix instruction, are what made it faster:
 // 32x32x32 products 516 us, 16x16x64 450, whole-line stores past the caches 427, every
-// lambda inlined 404. Half lines (64 bytes of depth per step, four or five buffers)
+// lambda inlined 408. Half lines (64 bytes of depth per step, four or five buffers)
 // and requests of lines ahead into the L2 were slower (556, 490).
-// 128 groups of 32768 x 4096 x 4096 (mean 256 rows, up to 1300): 751 us: weights of
+// 128 groups of 32768 x 4096 x 4096 (mean 256 rows, up to 1300): 756 us: weights of
 // 2.1 GB, read by 1.5 M-tiles each, and the matrix work of partly filled tiles.
 template <typename T, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int ntiles) {
@@ -641,7 +641,7 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 // bound by the time of one block. Columns N = 4096, depth 7168, bf16, in us from
 // call to call (a call takes the host 9 to 10 us):
 //   rows      256x256  128x256  128x128  64x128  64x32  32x32  16x32  16x16
-//   16384         404      490
+//   16384         408      490
 //    2048          92       65       79
 //    1024          91       57       44      59
 //     512          91       56       40      32     92
