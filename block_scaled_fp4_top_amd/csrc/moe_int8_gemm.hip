@@ -501,9 +501,14 @@ static int cu_count() {
     return c;
 }
 
+// M-tiles there can be: whole ones, and a last one for each expert with rows.
+static int64_t most_mtiles(const Int8Args& p, int bm) {
+    return p.offsets ? p.M / bm + std::min(p.E, p.M) : (p.M + bm - 1) / bm;
+}
+
 template <typename T, int BM, int BN, int WM, int WN, int S>
 static void launch_wide(const Int8Args& p, hipStream_t s) {
-    const int64_t mtiles = (p.M + BM - 1) / BM + (p.offsets ? p.E : 0), ntiles = (p.N + BN - 1) / BN;
+    const int64_t mtiles = most_mtiles(p, BM), ntiles = (p.N + BN - 1) / BN;
     const int64_t blocks = std::min<int64_t>(std::max(cu_count(), 8), mtiles * ntiles);
     hipLaunchKernelGGL((int8_wide_kernel<T, BM, BN, WM, WN, S>), dim3((unsigned)((blocks + 7) / 8 * 8)),
                        dim3(WM * WN * 64), 0, s, p, (int)ntiles);
@@ -631,7 +636,7 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int nt
 
 template <typename T, int MS, int NS, int NW, int P>
 static void launch_narrow(const Int8Args& p, hipStream_t s) {
-    const int64_t mtiles = (p.M + MS * 16 - 1) / (MS * 16) + (p.offsets ? p.E : 0), ntiles = (p.N + NS * 16 - 1) / (NS * 16);
+    const int64_t mtiles = most_mtiles(p, MS * 16), ntiles = (p.N + NS * 16 - 1) / (NS * 16);
     hipLaunchKernelGGL((int8_narrow_kernel<T, MS, NS, NW, P>), dim3((unsigned)((mtiles * ntiles + 7) / 8 * 8)),
                        dim3(NW * 64), 0, s, p, (int)ntiles);
 }

@@ -495,7 +495,7 @@ GROUPED = [  # T, K, N, depth, E, drop, skew
     (128, 1, 64, 2048, 100, False, False), (9, 64, 48, 32, 7, True, False), (700, 6, 257, 1040, 2, False, False),
     # the wide tiles: 64x128, 128x128, 128x256 (many and few rows), 256x256, with empty and ragged groups
     (90, 6, 1301, 208, 10, True, False), (160, 6, 1902, 336, 16, True, True), (300, 4, 3003, 144, 20, False, False),
-    (40, 8, 2050, 272, 60, False, True), (1200, 4, 2403, 208, 12, False, False), (1100, 4, 2302, 400, 12, True, True)]
+    (1, 8, 1000, 64, 1024, False, False), (3, 8, 70, 32, 1000, True, False), (40, 8, 2050, 272, 60, False, True), (1200, 4, 2403, 208, 12, False, False), (1100, 4, 2302, 400, 12, True, True)]
 
 
 @pytest.mark.parametrize("dtype", DT, ids=NAME.get)
