@@ -62,7 +62,9 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sb, float bias)
     return __fmaf_rn((float)sum * (big ? sb : sa), big ? sa : sb, bias);
 }
 
-// Rows of expert e. Offsets are clamped to [0, M], so a damaged list stays in range.
+// Rows of expert e. Offsets are clamped to [0, M], so a damaged list stays in range. (One
+// that goes back lets experts share rows: there may then be more tiles than most_mtiles
+// says, and the kernels leave out those behind.)
 __device__ __forceinline__ void expert_rows(const Int8Args& p, int e, int* lo, int* hi) {
     *lo = *hi = 0;
     if (e < p.E) {
@@ -196,7 +198,7 @@ constexpr uint32_t kOutOfRange = 0xFFFF0000u;
 // 128 groups of 32768 x 4096 x 4096 (mean 256 rows, up to 1300): 756 us: weights of
 // 2.1 GB, read by 1.5 M-tiles each, and the matrix work of partly filled tiles.
 template <typename T, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int ntiles) {
+__global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int most_mtiles, int ntiles) {
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
     constexpr int BK = 128, SL = BK / 64;               // bytes of depth per step, slices per step
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // 1 KB loads of A and of B per wave and step
@@ -218,9 +220,11 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int
             expert_rows(p, base + lane, &lo, &hi);
             const int n = (hi - lo + BM - 1) / BM;
             const int incl = wave_incl_scan(n);
-            if (base + lane < p.E) s_first[base + lane] = mtiles + incl - n;
+            if (base + lane < p.E) s_first[base + lane] = min(mtiles + incl - n, most_mtiles);
             mtiles += __builtin_amdgcn_readlane(incl, 63);
         }
+        // (the host has checked that most_mtiles * ntiles fits 32 bits)
+        mtiles = min(mtiles, most_mtiles);
     }
     // Tile order: one contiguous range per XCD (blocks are dealt to the 8 XCDs in
     // turn), dealt to the XCD's blocks in turn. Inside it expert by expert, and there
@@ -525,7 +529,7 @@ static void launch_wide(const Int8Args& p, hipStream_t s) {
     const int64_t mtiles = most_mtiles(p, BM), ntiles = (p.N + BN - 1) / BN;
     const int64_t blocks = std::min<int64_t>(std::max(cu_count(), 8), mtiles * ntiles);
     hipLaunchKernelGGL((int8_wide_kernel<T, BM, BN, WM, WN, S>), dim3((unsigned)((blocks + 7) / 8 * 8)),
-                       dim3(WM * WN * 64), 0, s, p, (int)ntiles);
+                       dim3(WM * WN * 64), 0, s, p, (int)mtiles, (int)ntiles);
 }
 
 // ---------------------------------------------------------------------------
@@ -537,15 +541,15 @@ static void launch_wide(const Int8Args& p, hipStream_t s) {
 // operands on their way straight into its registers, and the waves' integer sums
 // are joined through the LDS, which is exact in any order.
 template <typename T, int MS, int NS, int NW, int P>
-__global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int ntiles) {
+__global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int most_mtiles, int ntiles) {
     constexpr int BM = MS * 16, BN = NS * 16;
     __shared__ __attribute__((aligned(16))) i32x4 part[NW][MS * NS][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, quad = lane >> 4;
     // one contiguous range of tiles per XCD, M-tiles of a column block side by side
-    const int mtiles = count_tiles<BM>(p, lane);
-    const int per = (int)(((int64_t)mtiles * ntiles + 7) >> 3), j8 = blockIdx.x >> 3;
+    const int mtiles = min(count_tiles<BM>(p, lane), most_mtiles);
+    const int per = (mtiles * ntiles + 7) >> 3, j8 = blockIdx.x >> 3;
     const int id = (blockIdx.x & 7) * per + j8;
     if (j8 >= per || id >= mtiles * ntiles) return;
     int e, row0, rows;
@@ -652,7 +656,7 @@ template <typename T, int MS, int NS, int NW, int P>
 static void launch_narrow(const Int8Args& p, hipStream_t s) {
     const int64_t mtiles = most_mtiles(p, MS * 16), ntiles = (p.N + NS * 16 - 1) / (NS * 16);
     hipLaunchKernelGGL((int8_narrow_kernel<T, MS, NS, NW, P>), dim3((unsigned)((mtiles * ntiles + 7) / 8 * 8)),
-                       dim3(NW * 64), 0, s, p, (int)ntiles);
+                       dim3(NW * 64), 0, s, p, (int)mtiles, (int)ntiles);
 }
 
 // The tile shape: the largest that still gives about one block per CU. A larger

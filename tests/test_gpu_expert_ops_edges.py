@@ -1,5 +1,5 @@
 """The operators around the experts at their edges, on the GPU: scales near the ends
-of fp32."""
+of fp32, and offsets that go back."""
 import numpy as np
 import pytest
 import torch
@@ -74,3 +74,30 @@ def test_scales_at_the_ends_of_fp32(M, N, K, E, dtype):
         assert bool((over | sure).mean() > 0.99) and (bool(over.any()) or M < 37)
         assert np.array_equal(got[over], np.copysign(np.inf, want[over])), "overflow"
         assert_within(torch.as_tensor(got[sure]), want[sure], stored(bound, want, dtype)[sure], f"bias={with_bias}")
+
+
+# ---------------------------------------------------------------------------
+# offsets that go back
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N", [8, 1300, 2050, 9000])  # narrow tiles, 64x128, 128x256 twice
+def test_offsets_that_go_back(N, gather):
+    """Every second expert claims all rows, which makes more tiles than an ascending list
+    can have. All experts hold the same matrix, so whichever writes a row, it is right;
+    nothing outside the rows is touched."""
+    say("offsets that go back", N, gather)
+    M, E, D = 600, 40, 80
+    g = torch.Generator(device=DEV).manual_seed(N)
+    a = torch.randint(-127, 128, (M, D), dtype=torch.int8, device=DEV, generator=g)
+    b = torch.randint(-127, 128, (N, D), dtype=torch.int8, device=DEV, generator=g)
+    off = torch.tensor([0, M] * (E // 2) + [0], dtype=torch.int32, device=DEV)
+    rows = torch.arange(M, dtype=torch.int32, device=DEV)
+    order = moe.RouteOrder(rows, rows, off, M, 1, E)
+    around = torch.full((M + 2, N + 4), 5.0, device=DEV)
+    one = torch.ones(1, device=DEV)
+    moe.int8_grouped_matmul(a, one.expand(M).contiguous(), b.expand(E, N, D), one.expand(E, N).contiguous(), order,
+                            gather=gather, out=around[1:-1, 2:-2])
+    want = (a.double() @ b.double().t().contiguous()).float()
+    assert torch.equal(around[1:-1, 2:-2], want)
+    around[1:-1, 2:-2] = 5
+    assert bool((around == 5).all())
