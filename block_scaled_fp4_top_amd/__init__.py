@@ -27,6 +27,9 @@ VIEWS = {"topk_ids": 0, "topk_w": 1, "counts": 2, "offsets": 3, "row_to_route": 
 STAGES = ["route", "permute", "quantize_x", "fc1", "quantize_fc2_input", "fc2", "finalize"]
 
 
+_MOST = (1 << 31) - 1  # the library takes sizes as int32, which ctypes would cut off silently
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe_fp4 error {code}: {msg}")
@@ -242,6 +245,8 @@ def finalize(permuted_out: torch.Tensor, route_to_row: torch.Tensor, weights, T:
         raise TypeError("permuted_out must be float32 or bfloat16")
     _need(permuted_out, "permuted_out", permuted_out.dtype)
     R, H = permuted_out.shape
+    if R > _MOST or H > _MOST:
+        raise ValueError(f"permuted_out has shape {tuple(permuted_out.shape)}, sizes must fit 32 bits")
     if R != T * K:
         raise ValueError(f"permuted_out has {R} rows, expected T*K = {T * K}")
     _need(route_to_row, "route_to_row", torch.int32, (T * K,), permuted_out.device)
@@ -262,6 +267,8 @@ def quantize(v: torch.Tensor, kind: str, stream=None):
     tensors (g is None for MXFP8)."""
     _need(v, "v", torch.float32)
     rows, cols = v.shape
+    if rows > _MOST or cols > _MOST:
+        raise ValueError(f"v has shape {tuple(v.shape)}, sizes must fit 32 bits")
     k = {"nvfp4_tensor": 0, "nvfp4_row": 1, "mxfp8": 2, "nvfp4_row_4o6": 3}[kind]
     dev = v.device
     if k == 2:
@@ -365,6 +372,8 @@ def _matrix(t, name, dtype, index, rows=None, cols=None):
     if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                          f"[{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]")
+    if shape[0] > _MOST or shape[1] > _MOST:
+        raise ValueError(f"{name} has shape {tuple(shape)}, sizes must fit 32 bits")
     ld, inner = t.stride()
     if inner != 1 and shape[1] != 1:
         raise ValueError(f"the elements of a row of {name} must be contiguous")
@@ -396,6 +405,8 @@ class RouteOrder:
 
     def __init__(self, row_to_route: torch.Tensor, route_to_row: torch.Tensor, offsets: torch.Tensor,
                  T: int, K: int, E: int):
+        if max(T, K, E, T * K) > _MOST:
+            raise ValueError(f"T={T}, K={K}, E={E}: sizes must fit 32 bits")
         _need(offsets, "offsets", torch.int32, (E + 1,))
         _need(row_to_route, "row_to_route", torch.int32, (T * K,), offsets.device)
         _need(route_to_row, "route_to_row", torch.int32, (T * K,), offsets.device)
@@ -436,6 +447,8 @@ def sort_routes(ids: torch.Tensor, E: int, stream=None) -> RouteOrder:
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     T, K = ids.shape
+    if T > _MOST or K > _MOST or abs(E) > _MOST:
+        raise ValueError(f"T={T}, K={K}, E={E}: sizes must fit 32 bits")
     n = _lib.moe_sort_workspace_bytes(T, K, E)
     if n == 0:
         raise MoeError(1, _lib.moe_last_error().decode())
@@ -627,6 +640,8 @@ def int8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
     if b.get_device() != dev:
         raise ValueError(f"b is on {b.device}, expected cuda:{dev}")
     N = b.shape[1]
+    if N > _MOST:
+        raise ValueError(f"b has shape {tuple(b.shape)}, sizes must fit 32 bits")
     be, ldb, inner = b.stride()
     if inner != 1 and K != 1:
         raise ValueError("the elements of a row of b must be contiguous")
