@@ -722,6 +722,8 @@ static int run_int8_matmul(Int8Args p, int out_dtype, bool grouped, hipStream_t 
     const int64_t far = (int64_t)1 << 23;  // 256 rows of a tile are addressed by 32-bit offsets
     if ((p.a_rows > 1 && p.lda > far) || (p.N > 1 && p.ldb > far) || (p.M > 1 && p.ldy > ((int64_t)1 << 31)))
         return reject(MOE_ERR_UNSUPPORTED, "a row stride above 2^23 bytes (a, b) or 2^31 elements (y)");
+    if (grouped && p.E > 1 && p.b_expert > ((int64_t)1 << 48))
+        return reject(MOE_ERR_UNSUPPORTED, "experts more than 2^48 bytes apart");
     if (p.row_to_route && (int64_t)(p.a_rows - 1) * p.lda + p.Kd > (int64_t)kOutOfRange)
         return reject(MOE_ERR_UNSUPPORTED, "gathered rows of 4 GiB or more");
     const int64_t most = ((int64_t)(p.M + 15) / 16 + (grouped ? p.E : 0)) * ((p.N + 15) / 16);

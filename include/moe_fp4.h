@@ -310,8 +310,8 @@ int moe_int_matmul(const int8_t* a, int64_t a_stride, const float* a_scales, con
 
 /* The same product expert by expert on sorted rows: the rows offsets[e] ..
  * offsets[e+1]-1 of y use b[e] ([E][N][K], experts b_expert_stride bytes
- * apart), b_scales[e] ([E][N]) and bias[e] ([E][N] or NULL). Rows of y outside
- * the offsets are left as they were.
+ * apart: a multiple of 16 from 0, one matrix for all, to 2^48), b_scales[e] ([E][N])
+ * and bias[e] ([E][N] or NULL). Rows of y outside the offsets are left as they were.
  *   row_to_route NULL: row r of y uses row r of a (a_rows = M).
  *   Otherwise row r uses row row_to_route[r] / topk of a, the token's (a_rows =
  *   M / topk tokens, below 4 GiB): FC1 needs no dispatched copy. Rows whose

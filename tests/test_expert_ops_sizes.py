@@ -1,6 +1,8 @@
 """The binding of the operators around the experts refuses sizes that its int32
 arguments cannot hold, instead of taking them modulo 2^32 (no GPU needed; on one, the
 public calls)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -22,6 +24,17 @@ def test_orders():
     for T, K, E in ((FAR, 1, 8), (1, FAR, 8), (0, FAR, 8), (4, 2, FAR), (1 << 20, 1 << 12, 8)):
         with pytest.raises(ValueError, match="32 bits"):
             moe.RouteOrder(empty, empty, empty, T, K, E)
+
+
+def test_experts_far_apart():
+    """A stride whose product with the experts wraps 64 bits hid an output that overlaps
+    the weights, and every other check behind it."""
+    a, sa, b, sb, off, y = (ctypes.c_void_p((i + 1) << 32) for i in range(6))  # far apart, never read
+    def call(E, stride, y=y):
+        return moe._lib.moe_int_grouped_matmul(a, 64, sa, 4, b, 64, stride, sb, None, off, None, 1, 4, 8, 64, E, 0, y, 8, None)
+    for stride in (1 << 62, (1 << 48) + 16):
+        assert call(3, stride) == 2 and b"apart" in moe._lib.moe_last_error()
+    assert call(3, 1 << 48, y=b) == 1 and call(1, 1 << 62, y=b) == 1 and b"overlaps" in moe._lib.moe_last_error()
 
 
 def test_layer_calls(monkeypatch):
