@@ -597,13 +597,17 @@ __global__ __launch_bounds__(NW * 64) void int8_narrow_kernel(Int8Args p, int mo
     for (int j = 0; j < NS; ++j)
 #pragma unroll
         for (int i = 0; i < MS; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+    // B stays cacheable: column blocks with several M-tiles share it, and weights that the
+    // last-level cache still holds come from there. Non-temporal loads took 11.2 us instead
+    // of 9.6 for 16 x 4096 x 7168, 18.9 instead of 16.3 with 64 rows, and from memory 12.0
+    // instead of 11.8 and 19.7 instead of 19.0.
     auto load = [&](int st, int k) INLINE {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const bool in = k + s * 64 + quad * 16 < p.Kd;
 #pragma unroll
             for (int j = 0; j < NS; ++j)
-                fb[st][s][j] = in ? __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(bp[j] + k + s * 64)) : i32x4{0, 0, 0, 0};
+                fb[st][s][j] = in ? *reinterpret_cast<const i32x4*>(bp[j] + k + s * 64) : i32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < MS; ++i)
                 fa[st][s][i] = in ? *reinterpret_cast<const i32x4*>(ap[i] + k + s * 64) : i32x4{0, 0, 0, 0};
@@ -664,23 +668,27 @@ static void launch_narrow(const Int8Args& p, hipStream_t s) {
 // bound by the time of one block. Columns N = 4096, depth 7168, bf16, in us from
 // call to call (a call takes the host 9 to 10 us):
 //   rows      256x256  128x256  128x128  64x128  64x32  32x32  16x32  16x16
-//   16384         408      490
-//    2048          92       65       79
-//    1024          91       57       44      59
-//     512          91       56       40      32     92
-//     256          90       56       39      31     50
-//     128          63       56       39      30     27     35
-//      64                             29      30     28     20     26
-//      32                             26             22     21     16     19
-//      16                             26             19     18     17     12
-// For experts the host knows the mean rows only: 64 tokens with 8 of 256 experts,
-// depth 7168: 758 us with 128x256 (6.0 TB/s of weights), 1044 or more with 16 rows;
+//   16384         409      459
+//    2048          82       58       67
+//    1024          81       51       36      48
+//     512          81       51       33      27     86
+//     256          91       51       32      25     44
+//     128          79       58       39      25     24     30
+//      64                             29      30     23     17     22
+//      32                             25             19     16     13     16
+//      16                             23             17     14     13     10
+// (weights of 29 MB that are still in the last-level cache; from memory the narrow
+// tiles take 2 to 3 us more, in the same order.) For experts the host knows an upper
+// bound of the mean rows only: the rows of dropped routes are among M. Without any, 64
+// tokens with 8 of 256 experts, depth 7168: 685 us with 128x256, 1044 or more with 16 rows;
 // 256-row tiles pay from about 192 mean rows on (128: 576 against 521 us, 1536: 482
-// against 528). Narrow tiles are no higher than the rows: 16 x 7168 x 7168 takes 18 us
-// with 16x32 and 19 with 64x32, 32 rows 21 with 32x32 and 23 with 64x32. A single
-// token's rows are broadcast, which favours 16x16 (1 x 14336 x 4096: 14.7 us, 64x128
-// 16.2; with 16 rows 20.6 and 17.2) until the wide tiles fill the CUs (1 x 28672 x
-// 8192: 46.9 and 45.9).
+// against 528). With 32 of 256 experts here and 4096 x 4096 weights the rule takes 256x256
+// for 4096 tokens, 164 us (128x256: 142), and 2048 tokens, 146 (128x128: 115), as for eight
+// times the rows. Narrow tiles are no higher than the rows: 16 x 7168 x 7168 takes 13 us
+// with 16x32 and 17 with 64x32, 32 rows 17 with 32x32 and 19 with 64x32. A single
+// token's rows are broadcast, which favours 16x16 (1 x 14336 x 4096: 13.6 us, 64x128
+// 16.8; with 16 rows both 17.9) until the wide tiles fill the CUs (1 x 28672 x 8192: 43.4
+// and 41.8).
 template <typename T>
 static hipError_t launch_int8_matmul(const Int8Args& p, hipStream_t s) {
     const int64_t groups = p.offsets ? std::min(p.E, p.M) : 1;
