@@ -322,7 +322,8 @@ def stage_times():
 # gradients, and 8-bit integer products. They run on the tensors' device, on
 # `stream` or that device's current stream; what they allocate belongs to that
 # stream. Matrices may have any row stride; the elements of a row are
-# contiguous. Gradients are functions of their own (autograd records nothing).
+# contiguous. Gradients are functions of their own: autograd records nothing, and a
+# result requires no gradient whatever its inputs require.
 # (Small calls are bound by the host, so what a call has made itself is not
 # checked again.)
 # ---------------------------------------------------------------------------

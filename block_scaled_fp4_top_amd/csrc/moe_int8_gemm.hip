@@ -130,7 +130,7 @@ struct __attribute__((packed, aligned(sizeof(T)))) Few {
 // Direct buffer -> LDS load of 16 bytes per lane from `base` + `off` (zeros from
 // `bytes` on): lane l's bytes land at dst + 16 l (dst is uniform across the wave).
 // ONCE: a non-temporal load, for lines that are read once: the rows of B of an
-// expert with one M-tile. 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us;
+// expert with one M-tile. 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us then;
 // mean rows of 16, 48, 64, 128 over 128 experts of 4096 x 4096 359 -> 325, 406 -> 377,
 // 422 -> 404, 516 -> 504 (with all of B non-temporal 326, 391, 443, 540: experts with
 // several tiles then lose their L2).
@@ -186,17 +186,18 @@ constexpr uint32_t kOutOfRange = 0xFFFF0000u;
 //    loads of whole 128-byte lines.
 //  - The first S steps of the next tile are requested between a tile's last step
 //    and its epilogue.
-// 16384 x 4096 x 7168 in bf16 with 256 x 256 tiles: 408 us, 2.36 POP/s (the plain
-// library product of that size: 465 us, 2.07). Built up to whole-line stores it took
-// 340 us without its loads and 366 without its products; neither the matrix cores
-// (51 % busy) nor the LDS (no bank conflicts) are full, the chip is at its power limit
-// (1.7 - 1.95 GHz instead of 2.4), which is why fewer bytes through the LDS and the
-// L2 per product, and the cheaper matrix instruction, are what made it faster:
-// 32x32x32 products 516 us, 16x16x64 450, whole-line stores past the caches 427, every
-// lambda inlined 408. Half lines (64 bytes of depth per step, four or five buffers)
+// 16384 x 4096 x 7168 in bf16 with 256 x 256 tiles: 405 to 431 us from card to card,
+// 2.2 to 2.4 POP/s (the plain library product of that size: 465 us, 2.07). Built up to
+// whole-line stores it took 340 us without its loads and 366 without its products;
+// neither the matrix cores (54 % busy) nor the LDS (no bank conflicts) are full, the chip
+// is at its power limit (1.7 - 2.0 GHz instead of 2.4), which is why fewer bytes through
+// the LDS and the L2 per product, and the cheaper matrix instruction, are what made it
+// faster: 32x32x32 products 516 us, 16x16x64 450, whole-line stores past the caches 427,
+// every lambda inlined 408. Half lines (64 bytes of depth per step, four or five buffers)
 // and requests of lines ahead into the L2 were slower (556, 490).
-// 128 groups of 32768 x 4096 x 4096 (mean 256 rows, up to 1300): 756 us: weights of
-// 2.1 GB, read by 1.5 M-tiles each, and the matrix work of partly filled tiles.
+// 128 groups of 32768 x 4096 x 4096 (mean 256 rows, up to 1300): 750 to 775 us: weights
+// of 2.1 GB, read by 1.5 M-tiles each (of the second readings about 60 % miss the L2),
+// and the matrix work of partly filled tiles.
 template <typename T, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM * WN * 64) void int8_wide_kernel(Int8Args p, int most_mtiles, int ntiles) {
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;

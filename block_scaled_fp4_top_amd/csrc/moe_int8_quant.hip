@@ -26,7 +26,7 @@ __device__ __forceinline__ int int8_code_exact(float x, float s, float inv) {
 // One row per TPT threads (a wave, or a block of 256), read once: each thread keeps
 // up to NV vectors of 16 bytes in registers between the maximum and the rounding
 // (LONG: rows of any length, read twice). Bound by memory: 16384 x 7168 bf16
-// (352 MB) takes 78 us, 4.5 TB/s.
+// (352 MB) takes 66 us, 5.3 TB/s.
 template <typename T, int TPT, int NV, bool LONG>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(const T* __restrict__ x, int64_t ld, int rows, int H,
                                                             int8_t* __restrict__ codes, int64_t ld_codes,
@@ -123,9 +123,10 @@ static hipError_t launch_int8_quantize(const T* x, int64_t ld, int rows, int H, 
 #define Q(TPT, NV, LONG)                                                                                       \
     hipLaunchKernelGGL((int8_quantize_kernel<T, TPT, NV, LONG>), dim3((rows + 256 / TPT - 1) / (256 / TPT)),   \
                        dim3(256), 0, s, x, ld, rows, H, codes, ld_codes, scales)
-    // a wave per row for many rows of up to 256 vectors (16384 x 2048 bf16: 25 us against
-    // 36 with a block per row), a block for few (256 x 2048: 5.6 us against 6.7) and
-    // for longer rows (16384 rows of 512 vectors: 40 against 48 us, of 896: 78 against 126)
+    // a wave per row for many rows of up to 256 vectors, a block for few and for longer
+    // ones. bf16 in a graph, us, with a wave (with a block): 16384 x 1024 12.3 (17.6), x 1536
+    // 17.2 (19.9), x 2048 25.5 (25.0), 65536 x 2048 77 (87); 4096 x 1024 5.2 (6.2), x 1536 7.7
+    // (7.4), x 2048 9.8 (8.4); 256 x 2048 6.4 (3.3); 16384 x 4096 46 (34), x 7168 97 (66)
     const bool wave = vecs <= 64 || (vecs <= 256 && rows >= 4096);
     if (wave && vecs <= 64) Q(64, 1, false);
     else if (wave && vecs <= 128) Q(64, 2, false);

@@ -291,7 +291,8 @@ int moe_combine_grad(const void* dy, int64_t dy_stride, int32_t dtype, const int
 /* Symmetric 8-bit quantization of each row: scales[m] = max_j |x[m,j]| / 127 in
  * fp32, codes[m,j] = x[m,j] / scales[m] rounded to the nearest integer, ties to
  * even (the exact quotient of the fp32 scale, so the codes are reproducible bit
- * for bit), in [-127, 127]. A zero row has scale 0 and codes 0; a row with an
+ * for bit), in [-127, 127]. A zero row has scale 0 and codes 0, and so has one whose
+ * scale rounds to 0 (its largest value is below 64 * 2^-149); a row with an
  * infinity or a NaN has that as its scale and codes 0 (products with it are NaN).
  *   x: [rows][cols] of type dtype, codes: [rows][cols].  1 <= cols <= 2^20,
  *   rows <= 2^23. */
