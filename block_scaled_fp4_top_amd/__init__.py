@@ -48,6 +48,7 @@ def _load():
             "(hipcc --offload-arch=gfx950)")
     L = ctypes.CDLL(_LIB_PATH)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    f32 = ctypes.c_float
     D = ctypes.POINTER(_Dims)
     sig = {
         "moe_prepared_bytes": (sz, [D]),
@@ -75,6 +76,17 @@ def _load():
         "moe_int_matmul": (ctypes.c_int, [P, i64, P, P, i64, P, P, i32, i32, i32, i32, P, i64, P]),
         "moe_int_grouped_matmul": (ctypes.c_int, [P, i64, P, i32, P, i64, i64, P, P, P, P, i32, i32,
                                                   i32, i32, i32, i32, P, i64, P]),
+        "moe_route": (ctypes.c_int, [P, i64, i32, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]),
+        "moe_route_grad": (ctypes.c_int, [P, P, i64, i32, P, i32, i32, i32, i32, i32, f32, P, i64, P]),
+        "moe_rms_norm": (ctypes.c_int, [P, i64, P, i64, i32, P, i32, i32, i32, f32, P, i64, P, i64, P, i64, P, P]),
+        "moe_rms_norm_grad_workspace_bytes": (sz, [i32, i32]),
+        "moe_rms_norm_grad": (ctypes.c_int, [P, i64, P, i64, i32, P, i32, P, i64, i32, i32, f32, P, sz, P, i64, P, P]),
+        "moe_activate": (ctypes.c_int, [P, i64, i32, i32, i32, i32, P, i32, P, P, P, i64, P]),
+        "moe_activate_int": (ctypes.c_int, [P, i64, i32, i32, i32, i32, P, i32, P, P, P, i64, P, P]),
+        "moe_activate_grad": (ctypes.c_int, [P, i64, P, i64, i32, i32, i32, i32, P, i32, P, P, P, P, i64, P, P]),
+        "moe_adapt_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "moe_adapt": (ctypes.c_int, [P, i64, P, i64, i32, P, P, P, P, i64, i64, P, i64, i64, P, i32, i32, i32, i32,
+                                     i32, P, sz, P, i64, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -89,7 +101,9 @@ EXPORTS = ["moe_prepared_bytes", "moe_prepare_weights", "moe_check_prepared",
            "moe_workspace_view", "moe_stage_timing", "moe_stage_times", "moe_last_error",
            "moe_sort_workspace_bytes", "moe_sort_routes", "moe_dispatch", "moe_dispatch_grad",
            "moe_combine", "moe_combine_grad", "moe_int_quantize", "moe_int_matmul",
-           "moe_int_grouped_matmul"]
+           "moe_int_grouped_matmul", "moe_route", "moe_route_grad", "moe_rms_norm",
+           "moe_rms_norm_grad_workspace_bytes", "moe_rms_norm_grad", "moe_activate", "moe_activate_int",
+           "moe_activate_grad", "moe_adapt_workspace_bytes", "moe_adapt"]
 
 
 def lib_path() -> str:
@@ -653,4 +667,334 @@ def int8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
                                        order.offsets.data_ptr(),
                                        order.row_to_route.data_ptr() if gather else None, order.K, M, N, K, E,
                                        dt, out.data_ptr(), ldy, _raw_stream(dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Operators in front of, between and beside the experts' products: routing, RMS norm,
+# activation, low-rank adapters. The same conventions as above.
+# ---------------------------------------------------------------------------
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _choice(table, key, name):
+    code = table.get(key) if isinstance(key, str) else None
+    if code is None:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}")
+    return code
+
+
+def _sizes(*sizes):
+    if max(sizes) > _MOST or min(sizes) < -_MOST:
+        raise ValueError(f"sizes {sizes} must fit 32 bits")
+
+
+def route(logits: torch.Tensor, K: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """The router's choice: (ids int32 [T, K], weights fp32 [T, K]) from logits [T, E].
+
+    score: "softmax" over the experts or "sigmoid". The K largest score + bias (bias [E]
+    fp32, in the choice only) are taken, descending, ties to the lower expert; with groups > 1
+    only from the top_groups groups of E / groups consecutive experts whose group_top (1 or
+    2) largest sum highest. weights: scale * score, divided by the sum of the chosen scores
+    if renormalize. Choices are compared exactly, not in rounded scores. Experts with a logit
+    or bias of -inf are never chosen: ids are -1 and weights 0 where fewer than K are left
+    (sort_routes drops them). A NaN makes its token's weights NaN."""
+    dev = _device_index(logits)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(route, (logits, K, score, bias, groups, top_groups, group_top, renormalize, scale), stream)
+    dt = _float_type(logits, "logits")
+    ld = _matrix(logits, "logits", logits.dtype, dev)
+    T, E = logits.shape
+    _sizes(K, T * K, groups, top_groups, group_top)
+    sc = SCORES.get(score)
+    if sc is None:
+        sc = _choice(SCORES, score, "score")
+    b = None if bias is None else _vector(bias, "bias", dev, (E,))
+    if K < 0:
+        raise ValueError(f"K={K} is negative")
+    both = torch.empty((2, T, K), dtype=torch.int32, device=logits.device)
+    p = both.data_ptr()
+    _check(_lib.moe_route(logits.data_ptr(), ld, dt, b, T, E, K, sc, groups, top_groups, group_top,
+                          1 if renormalize else 0, scale, p, p + 4 * T * K, _raw_stream(dev)))
+    ids, weights = both.unbind(0)
+    return ids, weights.view(torch.float32)
+
+
+def route_grad(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+               renormalize: bool = True, scale: float = 1.0, out=None, stream=None) -> torch.Tensor:
+    """Gradient of route's weights to the logits [T, E], in their type, from dweights [T, K]
+    fp32 (as combine_grad and dispatch_grad give it) and route's ids. The choice has no
+    gradient, so neither has the bias; an id outside [0, E) adds nothing."""
+    dev = _device_index(dweights)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(route_grad, (dweights, logits, ids, score, renormalize, scale, out), stream)
+    dt = _float_type(logits, "logits")
+    ld = _matrix(logits, "logits", logits.dtype, dev)
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be [{T}, K], got {tuple(ids.shape)}")
+    K = ids.shape[1]
+    _sizes(T * K)
+    dw = _vector(dweights, "dweights", dev, (T, K))
+    _need(ids, "ids", torch.int32, (T, K), logits.device)
+    if out is None:
+        out, ld_out = torch.empty((T, E), dtype=logits.dtype, device=logits.device), E
+    else:
+        ld_out = _matrix(out, "out", logits.dtype, dev, T, E)
+    _check(_lib.moe_route_grad(dw, logits.data_ptr(), ld, dt, ids.data_ptr(), T, E, K, _choice(SCORES, score, "score"),
+                               1 if renormalize else 0, scale, out.data_ptr(), ld_out, _raw_stream(dev)))
+    return out
+
+
+def _norm_weight(weight, x, H, dev):
+    """(address, type code) of a norm's weight: [H] of x's type or fp32, or None."""
+    if weight is None:
+        return None, 2
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    if weight.dtype is not x.dtype and weight.dtype is not torch.float32:
+        raise TypeError(f"weight must be {x.dtype} or torch.float32, got {weight.dtype}")
+    if weight.get_device() != dev:
+        raise ValueError(f"weight is on {weight.device}, expected cuda:{dev}")
+    if weight.shape != (H,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous and of shape [{H}], got {tuple(weight.shape)}")
+    return weight.data_ptr(), DTYPES[weight.dtype]
+
+
+def _norm(x, weight, eps, residual, total, y, codes, scales, dev, want_y, want_codes):
+    """Both forms of the norm: (y, codes, scales, total)."""
+    dt = _float_type(x, "x")
+    ld = _matrix(x, "x", x.dtype, dev)
+    T, H = x.shape
+    w, wdt = _norm_weight(weight, x, H, dev)
+    rp, ldr, tp, ldt = None, 0, None, 0
+    if residual is not None:
+        ldr, rp = _matrix(residual, "residual", x.dtype, dev, T, H), residual.data_ptr()
+        if total is None:
+            total, ldt = torch.empty((T, H), dtype=x.dtype, device=x.device), H
+        else:
+            ldt = _matrix(total, "total", x.dtype, dev, T, H)
+        tp = total.data_ptr()
+    elif total is not None:
+        raise ValueError("total is the sum with the residual, which is missing")
+    yp, ldy, cp, ldc, sp = None, 0, None, 0, None
+    if y is not None:
+        ldy, yp = _matrix(y, "y" if want_codes else "out", x.dtype, dev, T, H), y.data_ptr()
+    elif want_y:
+        y, ldy = torch.empty((T, H), dtype=x.dtype, device=x.device), H
+        yp = y.data_ptr()
+    if want_codes:
+        if codes is None:
+            codes, ldc = torch.empty((T, H), dtype=torch.int8, device=x.device), H
+        else:
+            ldc = _matrix(codes, "out", torch.int8, dev, T, H)
+        if scales is None:
+            scales = torch.empty(T, dtype=torch.float32, device=x.device)
+            sp = scales.data_ptr()
+        else:
+            sp = _vector(scales, "scales", dev, (T,))
+        cp = codes.data_ptr()
+    _check(_lib.moe_rms_norm(x.data_ptr(), ld, rp, ldr, dt, w, wdt if w else dt, T, H, eps, tp, ldt, yp, ldy, cp, ldc, sp,
+                             _raw_stream(dev)))
+    return y, codes, scales, x if residual is None else total
+
+
+def rms_norm(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=None, out=None, total=None, stream=None):
+    """Root-mean-square norm of each row: (y, h) with h = x + residual, rounded to x's type
+    (the new residual stream; x itself without a residual), and
+    y = h / sqrt(mean(h^2) + eps) * weight. x, residual: [T, H]; weight: [H] of x's type or
+    fp32, or None for ones. total: where to write h (it may be residual itself)."""
+    dev = _device_index(x)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(rms_norm, (x, weight, eps, residual, out, total), stream)
+    y, _, _, h = _norm(x, weight, eps, residual, total, out, None, None, dev, True, False)
+    return y, h
+
+
+def rms_norm_int8(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=None, y=None, out=None, scales=None,
+                  total=None, stream=None):
+    """rms_norm with an 8-bit result for the integer products: (codes int8 [T, H], scales fp32
+    [T], h). The codes are quantize_int8's of h * weight in fp32 (the norm's factor is one
+    of the row's, so it only enters the scales): they are reproducible bit for bit. y: a
+    tensor that gets rms_norm's y as well (for the router). out, scales, total: where to
+    write codes, scales and h."""
+    dev = _device_index(x)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(rms_norm_int8, (x, weight, eps, residual, y, out, scales, total), stream)
+    _, codes, scales, h = _norm(x, weight, eps, residual, total, y, out, scales, dev, False, True)
+    return codes, scales, h
+
+
+def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight=None, eps: float = 1e-6, dtotal=None, out=None, stream=None):
+    """Gradients of rms_norm: (dx [T, H], dweight fp32 [H] or None without a weight) from dy,
+    the gradient of y, h as rms_norm returned it, and dtotal, the gradient of h as the
+    residual stream (or None). dx is the gradient of x and of the residual."""
+    dev = _device_index(dy)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(rms_norm_grad, (dy, h, weight, eps, dtotal, out), stream)
+    dt = _float_type(dy, "dy")
+    ld = _matrix(dy, "dy", dy.dtype, dev)
+    T, H = dy.shape
+    ldh = _matrix(h, "h", dy.dtype, dev, T, H)
+    w, wdt = _norm_weight(weight, dy, H, dev)
+    tp, ldt = None, 0
+    if dtotal is not None:
+        ldt, tp = _matrix(dtotal, "dtotal", dy.dtype, dev, T, H), dtotal.data_ptr()
+    if out is None:
+        out, ld_out = torch.empty((T, H), dtype=dy.dtype, device=dy.device), H
+    else:
+        ld_out = _matrix(out, "out", dy.dtype, dev, T, H)
+    dw, n, ws, dwp = None, 0, None, None
+    if weight is not None:
+        n = _lib.moe_rms_norm_grad_workspace_bytes(T, H)
+        if n == 0:
+            raise MoeError(2, _lib.moe_last_error().decode())
+        dw = torch.empty(H, dtype=torch.float32, device=dy.device)
+        room = torch.empty(n, dtype=torch.uint8, device=dy.device)
+        ws, dwp = room.data_ptr(), dw.data_ptr()
+    _check(_lib.moe_rms_norm_grad(dy.data_ptr(), ld, h.data_ptr(), ldh, dt, w, wdt if w else dt, tp, ldt, T, H, eps, ws, n,
+                                  out.data_ptr(), ld_out, dwp, _raw_stream(dev)))
+    return out, dw
+
+
+def _act_rows(h, act, order, weights, dev):
+    """Checks what the activation's calls share: (type, row stride, act, rows, I, offsets, E, row_to_route, weights)."""
+    dt = _float_type(h, "h")
+    ld = _matrix(h, "h", h.dtype, dev)
+    code = ACTS.get(act)
+    if code is None:
+        code = _choice(ACTS, act, "act")
+    M, I = h.shape
+    if code == 0:
+        if I % 2:
+            raise ValueError(f"h must be [rows, 2 I] for swiglu, got {tuple(h.shape)}")
+        I //= 2
+    if order is None:
+        if weights is not None:
+            raise ValueError("weights need an order")
+        return dt, ld, code, M, I, None, 1, None, None
+    _order(order, dev)
+    if order.T * order.K != M:
+        raise ValueError(f"h has {M} rows, the order {order.T * order.K} routes")
+    w = None if weights is None else _vector(weights, "weights", dev, (order.T, order.K))
+    return dt, ld, code, M, I, order.offsets.data_ptr(), order.E, order.row_to_route.data_ptr() if weights is not None else None, w
+
+
+def activate(h: torch.Tensor, act: str = "swiglu", order=None, weights=None, out=None, stream=None) -> torch.Tensor:
+    """The activation between an expert's two products: "swiglu" silu(h[:, :I]) * h[:, I:] of
+    h [M, 2 I], or "relu2" max(h, 0)^2 of h [M, I]. order: h holds the sorted rows, of which
+    those from offsets[E] on are neither read nor written (uninitialised if out is
+    allocated here). weights [T, K] fp32 (with an order): each row times its route's."""
+    dev = _device_index(h)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(activate, (h, act, order, weights, out), stream)
+    dt, ld, code, M, I, off, E, r2r, w = _act_rows(h, act, order, weights, dev)
+    if out is None:
+        out, ld_out = torch.empty((M, I), dtype=h.dtype, device=h.device), I
+    else:
+        ld_out = _matrix(out, "out", h.dtype, dev, M, I)
+    _check(_lib.moe_activate(h.data_ptr(), ld, dt, code, M, I, off, E, r2r, w, out.data_ptr(), ld_out, _raw_stream(dev)))
+    return out
+
+
+def activate_int8(h: torch.Tensor, act: str = "swiglu", order=None, weights=None, out=None, scales=None, stream=None):
+    """activate with an 8-bit result for the integer products: (codes int8 [M, I], scales fp32
+    [M]). The codes are quantize_int8's of the activation in 64 bits, so they are
+    reproducible bit for bit; a route's weight only enters its row's scale."""
+    dev = _device_index(h)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(activate_int8, (h, act, order, weights, out, scales), stream)
+    dt, ld, code, M, I, off, E, r2r, w = _act_rows(h, act, order, weights, dev)
+    if out is None:
+        out, ld_out = torch.empty((M, I), dtype=torch.int8, device=h.device), I
+    else:
+        ld_out = _matrix(out, "out", torch.int8, dev, M, I)
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=h.device)
+        sp = scales.data_ptr()
+    else:
+        sp = _vector(scales, "scales", dev, (M,))
+    _check(_lib.moe_activate_int(h.data_ptr(), ld, dt, code, M, I, off, E, r2r, w, out.data_ptr(), ld_out, sp,
+                                 _raw_stream(dev)))
+    return out, scales
+
+
+def activate_grad(da: torch.Tensor, h: torch.Tensor, act: str = "swiglu", order=None, weights=None, out=None,
+                  stream=None):
+    """Gradients of activate: (dh of h's shape, dweights [T, K] fp32 or None without weights)
+    from da [M, I], the gradient of its result. dweights is 0 for a dropped route."""
+    dev = _device_index(da)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(activate_grad, (da, h, act, order, weights, out), stream)
+    dt, ld, code, M, I, off, E, r2r, w = _act_rows(h, act, order, weights, dev)
+    ld_da = _matrix(da, "da", h.dtype, dev, M, I)
+    wide = h.shape[1]
+    if out is None:
+        out, ld_out = torch.empty((M, wide), dtype=h.dtype, device=h.device), wide
+    else:
+        ld_out = _matrix(out, "out", h.dtype, dev, M, wide)
+    dw, rt2, dwp = None, None, None
+    if w is not None:
+        dw = torch.empty((order.T, order.K), dtype=torch.float32, device=h.device)
+        rt2, dwp = order.route_to_row.data_ptr(), dw.data_ptr()
+    _check(_lib.moe_activate_grad(da.data_ptr(), ld_da, h.data_ptr(), ld, dt, code, M, I, off, E, r2r, rt2, w,
+                                  out.data_ptr(), ld_out, dwp, _raw_stream(dev)))
+    return out, dw
+
+
+def _adapters(t, name, dtype, dev, n, rows, cols):
+    """Checks a 3-D tensor with contiguous rows; returns (adapter stride, row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or (rows is not None and shape[1] != rows) or (cols is not None and shape[2] != cols):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{n}, {'rank' if rows is None else rows}, "
+                         f"{'rank' if cols is None else cols}]")
+    be, ld, inner = t.stride()
+    if inner != 1 and shape[2] != 1:
+        raise ValueError(f"the elements of a row of {name} must be contiguous")
+    return be, ld
+
+
+def adapt(base: torch.Tensor, x: torch.Tensor, order: RouteOrder, a: torch.Tensor, b: torch.Tensor, scales=None,
+          out=None, stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection:
+    out[t] = base[t] + scales[e] * b[e] @ (a[e] @ x[t]), e the adapter of token t, and
+    out[t] = base[t] for a token without one. base [T, N] (the projection's result), x [T, H],
+    a [n, rank, H], b [n, N, rank], bfloat16 or float16; scales [n] fp32 or None for 1. order:
+    sort_routes(ids, n) of the tokens' adapters ids [T, 1], outside [0, n) for none. out may
+    be base. H is a multiple of 16, the rank one of 8 up to 256."""
+    dev = _device_index(base)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(adapt, (base, x, order, a, b, scales, out), stream)
+    dt = _float_type(base, "base")
+    ld = _matrix(base, "base", base.dtype, dev)
+    T, N = base.shape
+    _order(order, dev, T)
+    if order.K != 1:
+        raise ValueError(f"order has {order.K} routes a token, expected one adapter")
+    n = order.E
+    ldx = _matrix(x, "x", base.dtype, dev, T)
+    H = x.shape[1]
+    ae, lda = _adapters(a, "a", base.dtype, dev, n, None, H)
+    r = a.shape[1]
+    _sizes(r)
+    be, ldb = _adapters(b, "b", base.dtype, dev, n, N, r)
+    sp = None if scales is None else _vector(scales, "scales", dev, (n,))
+    if out is None:
+        out, ld_out = torch.empty((T, N), dtype=base.dtype, device=base.device), N
+    else:
+        ld_out = _matrix(out, "out", base.dtype, dev, T, N)
+    size = _lib.moe_adapt_workspace_bytes(T, n, H, r)
+    if size == 0:
+        raise MoeError(2, _lib.moe_last_error().decode())
+    ws = torch.empty(size, dtype=torch.uint8, device=base.device)
+    _check(_lib.moe_adapt(base.data_ptr(), ld, x.data_ptr(), ldx, dt, order.row_to_route.data_ptr(),
+                          order.route_to_row.data_ptr(), order.offsets.data_ptr(), a.data_ptr(), ae, lda, b.data_ptr(), be,
+                          ldb, sp, T, n, H, r, N, ws.data_ptr(), size, out.data_ptr(), ld_out, _raw_stream(dev)))
     return out

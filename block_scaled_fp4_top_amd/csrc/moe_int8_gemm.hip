@@ -9,7 +9,7 @@
 
 #include "moe_args.h"
 #include "moe_rows_dev.h"
-#include "moe_route_dev.h"
+#include "moe_tiles_dev.h"
 
 // for the kernels' lambdas: what one captures would go through scratch memory if it
 // were called
@@ -62,15 +62,8 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sb, float bias)
     return __fmaf_rn((float)sum * (big ? sb : sa), big ? sa : sb, bias);
 }
 
-// Rows of expert e. Offsets are clamped to [0, M], so a damaged list stays in range. (One
-// that goes back lets experts share rows: there may then be more tiles than most_mtiles
-// says, and the kernels leave out those behind.)
 __device__ __forceinline__ void expert_rows(const Int8Args& p, int e, int* lo, int* hi) {
-    *lo = *hi = 0;
-    if (e < p.E) {
-        *lo = min(max(p.offsets[e], 0), p.M);
-        *hi = min(max(p.offsets[e + 1], *lo), p.M);
-    }
+    expert_rows(p.offsets, p.E, p.M, e, lo, hi);
 }
 
 // Tiles are counted expert by expert, ceil(rows / BM) each. The host knows only
@@ -98,25 +91,7 @@ __device__ __forceinline__ bool find_tile(const Int8Args& p, int tile, int lane,
         *rows = min(BM, p.M - *row0);
         return *rows > 0;
     }
-    int before = 0;
-    for (int base = 0; base < p.E; base += 64) {
-        int lo, hi;
-        expert_rows(p, base + lane, &lo, &hi);
-        const int n = (hi - lo + BM - 1) / BM;
-        const int incl = wave_incl_scan(n);
-        const int excl = before + incl - n;
-        const uint64_t hit = __ballot(tile >= excl && tile < excl + n);
-        if (hit) {
-            const int src = __ffsll((unsigned long long)hit) - 1;
-            const int first = __builtin_amdgcn_readlane(lo, src) + (tile - __builtin_amdgcn_readlane(excl, src)) * BM;
-            *e_out = base + src;
-            *row0 = first;
-            *rows = min(BM, __builtin_amdgcn_readlane(hi, src) - first);
-            return true;
-        }
-        before += __builtin_amdgcn_readlane(incl, 63);
-    }
-    return false;
+    return find_tile<BM>(p.offsets, p.E, p.M, tile, lane, e_out, row0, rows);
 }
 
 // ---------------------------------------------------------------------------

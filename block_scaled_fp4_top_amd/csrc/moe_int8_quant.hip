@@ -1,27 +1,10 @@
 // Symmetric 8-bit integer quantization of each row:
 //   s[m] = fl32(max_j |x[m,j]| / 127),  c[m,j] = round(x[m,j] / s[m])
 #include "moe_args.h"
+#include "moe_int8_dev.h"
 #include "moe_rows_dev.h"
 
 namespace moe {
-
-// Codes are the correctly rounded quotients x / s of the row's fp32 scale s (ties
-// to even). q = x * fl(1/s) is within 127 * 2^-23 of the quotient, so rint(q) is
-// the code unless q lies within kNear of a half; there the sign of the exact
-// remainder x - n s (one fma: at most 24 bits remain) against s / 2 decides.
-constexpr float kNear = 2e-5f;            // > 127 * 2^-23
-constexpr float kRoundInt = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
-constexpr float kTinyScale = 1e-37f;      // 1/s overflows below 2^-128: such rows divide in fp64
-
-__device__ __forceinline__ int int8_code_exact(float x, float s, float inv) {
-    if (s < kTinyScale) return (int)fmin(fmax(rint((double)x / (double)s), -127.0), 127.0);
-    float n = __builtin_rintf(x * inv);
-    const float r2 = 2.0f * __fmaf_rn(-n, s, x);  // twice the remainder, exact
-    const bool odd = ((int)n) & 1;
-    if (r2 > s || (r2 == s && odd)) n += 1.0f;
-    else if (r2 < -s || (r2 == -s && odd)) n -= 1.0f;
-    return (int)n;
-}
 
 // One row per TPT threads (a wave, or a block of 256), read once: each thread keeps
 // up to NV vectors of 16 bytes in registers between the maximum and the rounding
@@ -70,47 +53,18 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const T* __restrict_
         top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
     }
     top = __builtin_amdgcn_readfirstlane(top);
-    const float s = __fdiv_rn(u2f(top), 127.0f);
-    if (at == 0) scales[m] = s;
-    // zero, infinity and NaN: codes 0, by a factor of 0 (and no careful rounding)
-    const bool plain = s > 0.0f && top < 0x7F800000u;
-    const bool tiny = plain && s < kTinyScale;
-    const float inv = plain && !tiny ? __fdiv_rn(1.0f, s) : 0.0f;
+    const Int8Row r = int8_row(top);
+    if (at == 0) scales[m] = r.s;
     auto put = [&](const Vec<T>& u, int c) {
-        uint32_t w[V / 4];
-        float far = 0.0f;
+        float f[V];
 #pragma unroll
-        for (int g = 0; g < V / 4; ++g) {
-            uint32_t b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float f = to_f32(u.e[4 * g + i]);
-                const float n = __fmaf_rn(f, inv, kRoundInt);
-                b[i] = f2u(n);
-                far = fmaxf(far, fabsf(__fmaf_rn(f, inv, -(n - kRoundInt))));
-            }
-            const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u);
-            w[g] = lo | (hi << 16);
-        }
-        if (!plain) {
-#pragma unroll
-            for (int g = 0; g < V / 4; ++g) w[g] = 0;
-        } else if (tiny || far > 0.5f - kNear) {
-#pragma unroll
-            for (int g = 0; g < V / 4; ++g) {
-                w[g] = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[g] |= (uint32_t)(int8_code_exact(to_f32(u.e[4 * g + i]), s, inv) & 0xFF) << (8 * i);
-            }
-        }
-        typedef uint32_t words __attribute__((ext_vector_type(V / 4), aligned(1)));
-        *reinterpret_cast<words*>(dst + (int64_t)c * V) = __builtin_bit_cast(words, w);
+        for (int i = 0; i < V; ++i) f[i] = to_f32(u.e[i]);
+        store_codes<V>(dst + (int64_t)c * V, int8_codes<V>(f, r));
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         if (at + j * TPT < whole) put(v[j], at + j * TPT);
-    if (at < tail) dst[whole * V + at] = plain ? (int8_t)int8_code_exact(to_f32(last), s, inv) : (int8_t)0;
+    if (at < tail) dst[whole * V + at] = r.plain ? (int8_t)int8_code_exact(to_f32(last), r.s, r.inv) : (int8_t)0;
     if (LONG)
         for (int c = at + NV * TPT; c < whole; c += TPT) put(load_vec(row + (int64_t)c * V), c);
 }

@@ -39,4 +39,25 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T>& v) {
     else *reinterpret_cast<words4_at2*>(p) = w;
 }
 
+// N consecutive elements (16 or 32 bytes of them) at any alignment of one, as floats.
+template <int N, typename T>
+__device__ __forceinline__ void load_floats(const T* p, float* f) {
+    constexpr int V = 16 / sizeof(T);
+    if constexpr (N < V) {  // 8 bytes of 16-bit elements
+        static_assert(N * sizeof(T) == 8, "half a vector");
+        typedef uint32_t words2_at2 __attribute__((ext_vector_type(2), aligned(2)));
+        struct Half { T e[N]; };
+        const Half h = __builtin_bit_cast(Half, *reinterpret_cast<const words2_at2*>(p));
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = to_f32(h.e[i]);
+    } else {
+#pragma unroll
+        for (int g = 0; g < N / V; ++g) {
+            const Vec<T> v = load_vec(p + g * V);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[g * V + i] = to_f32(v.e[i]);
+        }
+    }
+}
+
 }  // namespace moe

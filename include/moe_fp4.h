@@ -324,6 +324,131 @@ int moe_int_grouped_matmul(const int8_t* a, int64_t a_stride, const float* a_sca
                            int32_t K, int32_t E, int32_t out_dtype, void* y, int64_t y_stride,
                            hipStream_t stream);
 
+/* -------------------------------------------------------------------------
+ * Operators in front of, between and beside the experts' products
+ * -------------------------------------------------------------------------
+ * Under the same conventions: strides in elements, contiguous rows, any stride from 0
+ * on for an input's rows, outputs apart from inputs and from each other. */
+
+/* Root-mean-square norm of each row, with the residual's addition before it:
+ *   h = x + residual, rounded to `dtype` and stored in total (x itself where
+ *   residual is NULL; the two come together);
+ *   r = 1 / sqrt(mean_j h_j^2 + eps);   y_j = h_j r weight_j, rounded once.
+ * The norm reads h as it is stored. 8-bit output (codes and scales come together,
+ * beside y or instead of it; for moe_int_matmul): p_j = h_j weight_j rounded to fp32,
+ * s = max_j |p_j| / 127 in fp32, codes[j] = p_j / s as moe_int_quantize rounds it,
+ * scales = s r. So the codes do not depend on r and are reproducible bit for bit. A row
+ * whose p has an infinity or a NaN has codes 0 and a scale that is not finite.
+ *   x, residual, total, y: [rows][cols] of type dtype; weight: [cols] of type
+ *   weight_dtype (dtype or fp32), or NULL for ones. total may be residual itself
+ *   (same address and stride). 1 <= cols <= 32768, rows <= 2^23, eps >= 0 (a zero
+ *   row with eps = 0 is NaN). */
+int moe_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                 int32_t dtype, const void* weight, int32_t weight_dtype, int32_t rows,
+                 int32_t cols, float eps, void* total, int64_t total_stride, void* y,
+                 int64_t y_stride, int8_t* codes, int64_t codes_stride, float* scales,
+                 hipStream_t stream);
+
+/* Workspace bytes of moe_rms_norm_grad with dweight (0 if the sizes are invalid). */
+size_t moe_rms_norm_grad_workspace_bytes(int32_t rows, int32_t cols);
+
+/* Gradients of moe_rms_norm from dy, the gradient of y, and h (x, or total): with
+ * n = h r, g = dy weight
+ *   dx = r (g - n mean_j(g n)) + dtotal    (also the residual's gradient; dtotal: the
+ *                                           gradient of total, or NULL)
+ *   dweight = sum over the rows of dy n    (fp32, rows in a fixed order; or NULL)
+ *   workspace: >= moe_rms_norm_grad_workspace_bytes(rows, cols) bytes, 16-byte
+ *   aligned; may be NULL without dweight. */
+int moe_rms_norm_grad(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride,
+                      int32_t dtype, const void* weight, int32_t weight_dtype, const void* dtotal,
+                      int64_t dtotal_stride, int32_t rows, int32_t cols, float eps, void* workspace,
+                      size_t workspace_bytes, void* dx, int64_t dx_stride, float* dweight,
+                      hipStream_t stream);
+
+/* The activation between an expert's two products, on sorted rows (moe_act):
+ *   swiglu: a_j = silu(h_j) h_{I+j}, h: [rows][2I];  relu2: a_j = max(h_j, 0)^2, h: [rows][I]
+ *   out[m][j] = w a_j, rounded once to dtype, with w = weights[row_to_route[m]] (the
+ *   router's weight on the input side of the second product), 1 where weights is NULL.
+ *   offsets ([E+1]): only the rows below offsets[E] are read and written; NULL: all rows.
+ *   weights ([rows], i.e. [T][K]) need offsets and row_to_route; rows whose entry names
+ *   no route are then left as they were. 1 <= I <= 32768, rows <= 2^23. */
+int moe_activate(const void* h, int64_t h_stride, int32_t dtype, int32_t act, int32_t rows,
+                 int32_t I, const int32_t* offsets, int32_t E, const int32_t* row_to_route,
+                 const float* weights, void* out, int64_t out_stride, hipStream_t stream);
+
+/* The same with an 8-bit result for moe_int_grouped_matmul: codes of a by
+ * moe_int_quantize's rule, s = max_j |a_j| / 127 rounded to fp32, codes[j] = a_j / s to the
+ * nearest integer, both of the a_j in 64 bits (so the codes are reproducible bit for
+ * bit), and scales[m] = w s. A row with a value beyond fp32 or a NaN has codes 0 and a
+ * scale that is not finite. codes: [rows][I], scales: [rows]. */
+int moe_activate_int(const void* h, int64_t h_stride, int32_t dtype, int32_t act, int32_t rows,
+                     int32_t I, const int32_t* offsets, int32_t E, const int32_t* row_to_route,
+                     const float* weights, int8_t* codes, int64_t codes_stride, float* scales,
+                     hipStream_t stream);
+
+/* Gradients of moe_activate from da ([rows][I], the gradient of out): dh, of h's shape, and
+ * dweights[route] = <da, a> in fp32, 0 for a route without a row (NULL, or with weights
+ * and route_to_row). The same rows are read and written. */
+int moe_activate_grad(const void* da, int64_t da_stride, const void* h, int64_t h_stride,
+                      int32_t dtype, int32_t act, int32_t rows, int32_t I, const int32_t* offsets,
+                      int32_t E, const int32_t* row_to_route, const int32_t* route_to_row,
+                      const float* weights, void* dh, int64_t dh_stride, float* dweights,
+                      hipStream_t stream);
+
+/* The router's choice of K experts for each token.
+ *   score s = softmax over the token's logits, or sigmoid (moe_score); choice c = s + bias
+ *   (bias: [E] fp32 or NULL; it takes part in the choice only). The experts lie in
+ *   `groups` groups of E / groups; a group's score is the sum of its group_top (1 or 2)
+ *   largest choices, and the top_groups best groups take part. ids[t]: the K experts
+ *   with the largest c, descending, ties (of groups too) to the lower index.
+ *   weights[t][k] = scale s[ids[t][k]], divided by the sum of the chosen s if renormalize.
+ * Choices are compared as if computed exactly (in 64 bits), not in rounded scores. An
+ * expert whose logit or bias is -inf is never chosen; where fewer than K are left the
+ * other ids are -1 (moe_sort_routes drops them) with weight 0. A NaN among a token's
+ * logits makes its weights NaN (as a choice it counts as the lowest finite value), a NaN
+ * in the bias every token's.
+ *   logits: [T][E] of type dtype. 1 <= E <= 1024, 1 <= K <= min(E, 64), T*K <= 2^23,
+ *   groups divides E. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+int moe_route(const void* logits, int64_t logits_stride, int32_t dtype, const float* bias,
+              int32_t T, int32_t E, int32_t K, int32_t score, int32_t groups, int32_t top_groups,
+              int32_t group_top, int32_t renormalize, float scale, int32_t* ids, float* weights,
+              hipStream_t stream);
+
+/* Gradient of moe_route's weights to the logits, from dweights [T][K]: dlogits [T][E] of
+ * type dtype, written entirely. An id outside [0, E) and one whose logit is -inf add
+ * nothing; the choice itself (and so the bias) has no gradient. */
+int moe_route_grad(const float* dweights, const void* logits, int64_t logits_stride, int32_t dtype,
+                   const int32_t* ids, int32_t T, int32_t E, int32_t K, int32_t score,
+                   int32_t renormalize, float scale, void* dlogits, int64_t dlogits_stride,
+                   hipStream_t stream);
+
+/* Workspace bytes of moe_adapt (0 if the sizes are invalid). */
+size_t moe_adapt_workspace_bytes(int32_t T, int32_t adapters, int32_t H, int32_t rank);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[t] = base[t] + scales[e] b[e] (a[e] x[t]), e the adapter of token t, and
+ *   out[t] = base[t] (bit for bit) for a token without one. Sums and a[e] x[t] in fp32,
+ *   one rounding.
+ *   base, out: [T][N], x: [T][H], a: [adapters][rank][H], b: [adapters][N][rank], all of
+ *   type dtype (bf16 or fp16); rows of a and b a_stride and b_stride apart, adapters
+ *   a_adapter_stride and b_adapter_stride (0: one for all, to 2^48). scales: [adapters]
+ *   fp32, or NULL for 1.
+ *   row_to_token, token_to_row [T], offsets [adapters + 1]: the tokens sorted by adapter, as
+ *   moe_sort_routes gives them for ids [T][1] (an id outside [0, adapters): no adapter).
+ *   Entries of the maps that name no row or token stay in range; damaged maps leave rows
+ *   of out unwritten.
+ *   out may be base itself (same address and stride).
+ *   workspace: >= moe_adapt_workspace_bytes(T, adapters, H, rank) bytes, 16-byte aligned.
+ *   H a multiple of 16, rank a multiple of 8 up to 256 (MOE_ERR_UNSUPPORTED otherwise),
+ *   1 <= adapters <= 1024, T <= 2^22, H, N <= 2^20. */
+int moe_adapt(const void* base, int64_t base_stride, const void* x, int64_t x_stride, int32_t dtype,
+              const int32_t* row_to_token, const int32_t* token_to_row, const int32_t* offsets,
+              const void* a, int64_t a_adapter_stride, int64_t a_stride, const void* b,
+              int64_t b_adapter_stride, int64_t b_stride, const float* scales, int32_t T,
+              int32_t adapters, int32_t H, int32_t rank, int32_t N, void* workspace,
+              size_t workspace_bytes, void* out, int64_t out_stride, hipStream_t stream);
+
 /* Message for the last non-OK status returned on this thread. */
 const char* moe_last_error(void);
 
