@@ -57,8 +57,6 @@ __device__ __forceinline__ Silu silu_parts(float g) {
     return g >= 0.0f ? Silu{r, e * r} : Silu{e * r, r};  // (NaN: e is NaN)
 }
 
-// SWIGLU's activation, off by at most 2^-21 relative: exp 2 half steps (2^-23), its sum
-// and product, the reciprocal's 2^-23, g sig, and u: 8 * 2^-24. relu2 by 2^-24.
 template <bool SWIGLU>
 __device__ __forceinline__ float act_of(float g, float u) {
     if constexpr (SWIGLU) return g * silu_parts(g).sig * u;
@@ -117,14 +115,24 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_kernel(ActArgs p)
 // ---------------------------------------------------------------------------
 // s = fl32(max_j |a_j| / 127) and code_j = round(a_j / s), of the values a_j in 64 bits, so
 // that the codes are those of any implementation that is careful enough. fp32 values
-// (off by kActError at most) decide all but a few: the largest ones, of which the
-// maximum is taken in fp64, and those whose quotient lies next to a half, which are
-// computed again in fp64. Rows whose largest value is below kSmallAct (fp32 loses bits
-// there) are computed in fp64 altogether; one that fp32 has as 0 has scale 0.
-constexpr float kActError = 0x1p-20f;  // > 2^-21 (act_of), with the quotient's own roundings
+// decide all but a few: the largest ones, of which the maximum is taken in fp64, and those
+// whose quotient lies next to a half, which are computed again in fp64 (a vector of a
+// lane at a time, by as many lanes). Rows whose largest value is below kSmallAct (fp32 loses
+// bits there) are computed in fp64 altogether; one that fp32 has as 0 has scale 0.
+//
+// kActError, relative, from kDeep on: exp2's argument is off by 1.25 |g| half steps (2^-24), exp2
+// and the reciprocal by 2 each, 1 + e, both products and the quotient by 5.5 in all: 30
+// half steps at g = -16. Gates below kDeep go the exact way.
+constexpr float kActError = 0x1p-19f;
+constexpr float kDeep = -16.0f;
 constexpr float kSmallAct = 0x1p-90f;
-constexpr float kDeep = -80.0f;
 
+template <bool SWIGLU>
+__device__ __forceinline__ float act_fast(float g, float u) {
+    if constexpr (SWIGLU) return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+    const float z = fmaxf(g, 0.0f);
+    return g != g ? g : z * z;
+}
 template <bool SWIGLU>
 __device__ __forceinline__ double act_exact(double g, double u) {
     if constexpr (SWIGLU) {
@@ -135,25 +143,14 @@ __device__ __forceinline__ double act_exact(double g, double u) {
     return z * z;
 }
 
-// Largest of the lanes' doubles (0 for lanes without one, few of which have one).
-__device__ __forceinline__ double few_max(double v) {
-    double top = 0.0;
-    const uint64_t bits = __builtin_bit_cast(uint64_t, v);
-    for (uint64_t left = __ballot(v > 0.0); left; left &= left - 1) {
-        const int l = __ffsll((unsigned long long)left) - 1;
-        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)bits, l), hi = __builtin_amdgcn_readlane((int)(bits >> 32), l);
-        top = fmax(top, __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo));
-    }
-    return top;
-}
-
 template <typename T, bool SWIGLU, int TPT, int NV>
 __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActArgs p) {
     constexpr int V = 16 / sizeof(T), NW = RowThreads<TPT>::kWaves;
-    static_assert(NV * V <= 64, "a bit for each element");
+    static_assert(NV * V <= 64, "a lane for each of a lane's elements");
     __shared__ uint32_t s_top[2][NW];
     __shared__ double s_max[2][NW];
-    const int at = threadIdx.x % TPT, whole = p.I / V, tail = p.I - whole * V, n = kept_rows(p);
+    const int at = threadIdx.x % TPT, lane = threadIdx.x & 63, at0 = at - lane;  // at0: lane 0's
+    const int whole = p.I / V, tail = p.I - whole * V, n = kept_rows(p);
     int set = 0;
     for (int m = first_row<TPT>(); m < n; m += gridDim.x * RowThreads<TPT>::kPer) {
         float w = 1.0f;
@@ -177,19 +174,33 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActAr
             if (SWIGLU) u_last = h[p.I + whole * V + at];
         }
         float a[NV][V], a_last = 0.0f;
-        uint32_t top = 0;
+        uint32_t mine = 0, doubt = 0;  // the lane's largest |a|; its vectors to be computed again
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            float low = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 a[j][i] = 0.0f;
-                if (at + j * TPT < whole) a[j][i] = act_of<SWIGLU>(to_f32(g[j].e[i]), SWIGLU ? to_f32(u[j].e[i]) : 0.0f);
-                top = max(top, f2u(a[j][i]) & 0x7FFFFFFFu);
+                if (at + j * TPT < whole) {
+                    const float gv = to_f32(g[j].e[i]);
+                    a[j][i] = act_fast<SWIGLU>(gv, SWIGLU ? to_f32(u[j].e[i]) : 0.0f);
+                    if (SWIGLU) low = fminf(low, gv);
+                }
             }
-        if (at < tail) a_last = act_of<SWIGLU>(to_f32(g_last), SWIGLU ? to_f32(u_last) : 0.0f);
-        top = lanes_max(max(top, f2u(a_last) & 0x7FFFFFFFu));
+            if (SWIGLU && low < kDeep) doubt |= 1u << j;
+#pragma unroll
+            for (int i = 0; i < V; ++i) mine = max(mine, f2u(a[j][i]) & 0x7FFFFFFFu);
+        }
+        bool odd = doubt != 0;  // has elements that fp32 says too little about
+        if (at < tail) {
+            a_last = act_fast<SWIGLU>(to_f32(g_last), SWIGLU ? to_f32(u_last) : 0.0f);
+            odd |= SWIGLU && to_f32(g_last) < kDeep;
+            mine = max(mine, f2u(a_last) & 0x7FFFFFFFu);
+        }
+        if (odd) mine = max(mine, 1u);  // (fp32 may have had 0 for all of a row that is not)
+        uint32_t top = lanes_max(mine);
         if constexpr (NW > 1) {
-            if ((threadIdx.x & 63) == 0) s_top[set][threadIdx.x >> 6] = top;
+            if (lane == 0) s_top[set][threadIdx.x >> 6] = top;
             __syncthreads();
 #pragma unroll
             for (int v = 0; v < NW; ++v) top = max(top, s_top[set][v]);
@@ -197,30 +208,22 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActAr
         top = __builtin_amdgcn_readfirstlane(top);
         const float big = u2f(top);
         const bool plain = top < 0x7F800000u && top > 0, small = plain && big < kSmallAct;
-        // element e of this thread: column (at + (e / V) * TPT) * V + e % V, again from memory
-        auto exact = [&](int c) INLINE {
+        auto exact = [&](int c) INLINE {  // column c, again from memory
             return act_exact<SWIGLU>((double)to_f32(h[c]), SWIGLU ? (double)to_f32(h[p.I + c]) : 0.0);
         };
-        auto column = [&](int e) INLINE { return (at + (e / V) * TPT) * V + e % V; };
         float s = 0.0f;
-        uint64_t deep = 0;  // elements whose exp(g) is subnormal in fp32, and less exact for it
         if (plain) {
             const float near = small ? 0.0f : big * (1.0f - 2.0f * kActError);
-            uint64_t many = 0;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (at + j * TPT < whole) {
-                        if (fabsf(a[j][i]) >= near) many |= 1ull << (j * V + i);
-                        if (SWIGLU && to_f32(g[j].e[i]) < kDeep) deep |= 1ull << (j * V + i);
-                    }
-            many |= deep;
-            double most = at < tail && (fabsf(a_last) >= near || (SWIGLU && to_f32(g_last) < kDeep)) ? fabs(exact(whole * V + at)) : 0.0;
-            for (; many; many &= many - 1) most = fmax(most, fabs(exact(column(__ffsll((unsigned long long)many) - 1))));
-            most = few_max(most);
+            double most = 0.0;
+            // all elements of each lane that has one that may be the largest, a lane each
+            for (uint64_t left = __ballot(u2f(mine) >= near || odd); left; left &= left - 1) {
+                const int owner = at0 + __ffsll((unsigned long long)left) - 1, v = owner + (lane / V) * TPT;
+                if (lane < NV * V && v < whole) most = fmax(most, fabs(exact(v * V + lane % V)));
+                if (owner < tail && lane == 0) most = fmax(most, fabs(exact(whole * V + owner)));
+            }
+            most = lanes_max(most);
             if constexpr (NW > 1) {
-                if ((threadIdx.x & 63) == 0) s_max[set][threadIdx.x >> 6] = most;
+                if (lane == 0) s_max[set][threadIdx.x >> 6] = most;
                 __syncthreads();
 #pragma unroll
                 for (int v = 0; v < NW; ++v) most = fmax(most, s_max[set][v]);
@@ -232,41 +235,40 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActAr
         if (at == 0) p.scales[m] = w * s;
         const bool coded = plain && s > 0.0f;
         const float inv = coded && !small ? __fdiv_rn(1.0f, s) : 0.0f;
-        uint64_t again = deep;
-        auto doubtful = [&](float x) INLINE {
-            const float q = x * inv, off = fabsf(q - __builtin_rintf(q));
-            return fabsf(off - 0.5f) <= __fmaf_rn(fabsf(q), kActError, 0x1p-30f);
-        };
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (at + j * TPT < whole) {
                 Codes<V> c;
+                float far = 0.0f;  // distance from the code, and what the quotient may be off
 #pragma unroll
                 for (int k = 0; k < V / 4; ++k) {
                     uint32_t b[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        b[i] = f2u(__fmaf_rn(a[j][4 * k + i], inv, kRoundInt));
-                        if (doubtful(a[j][4 * k + i])) again |= 1ull << (j * V + 4 * k + i);
+                        const float x = a[j][4 * k + i], r = __fmaf_rn(x, inv, kRoundInt), code = r - kRoundInt;
+                        b[i] = f2u(r);
+                        far = fmaxf(far, __fmaf_rn(fabsf(code), kActError, fabsf(__fmaf_rn(x, inv, -code))));
                     }
                     c.w[k] = coded ? int8_word(b) : 0;
                 }
                 store_codes<V>(dst + (at + j * TPT) * V, c);
+                // (|code| is within a half of the quotient)
+                if (far > 0.5f - 1.5f * kActError || small) doubt |= 1u << j;
             }
         auto code_exact = [&](int c) INLINE {
             return (int8_t)(int)fmin(fmax(rint(exact(c) / (double)s), -127.0), 127.0);
         };
         if (at < tail) dst[whole * V + at] = coded ? code_exact(whole * V + at) : (int8_t)0;
-        if (!coded) again = 0;
-        if (coded && small) {
-            again = 0;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (at + j * TPT < whole) again |= ((1ull << V) - 1) << (j * V);
-        }
-        for (; again; again &= again - 1) {  // (behind this thread's own store of the vector)
-            const int c = column(__ffsll((unsigned long long)again) - 1);
-            dst[c] = code_exact(c);
+        if (!coded) doubt = 0;
+        if (uint64_t left = __ballot(doubt != 0)) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // behind the stores of the other lanes
+            do {
+                const int l = __ffsll((unsigned long long)left) - 1, j = __ffs(__builtin_amdgcn_readlane((int)doubt, l)) - 1;
+                const int c = (at0 + l + j * TPT) * V + lane;
+                if (lane < V) dst[c] = code_exact(c);
+                if (lane == l) doubt &= doubt - 1;
+                left = __ballot(doubt != 0);
+            } while (left);
         }
         set ^= 1;
     }
@@ -373,8 +375,8 @@ static hipError_t launch_act(const ActArgs& p, hipStream_t s) {
         else if (vecs <= 256) A(KERNEL, 256, 1);                                                                       \
         else if (vecs <= 512) A(KERNEL, 256, 2);                                                                       \
         else if (vecs <= 1024) A(KERNEL, 256, 4);                                                                      \
-        else if (vecs <= 4096) A(KERNEL, 1024, 4);                                                                     \
-        else A(KERNEL, 1024, 8);                                                                                       \
+        else if (V == 8 || vecs <= 4096) A(KERNEL, 1024, 4);                                                           \
+        else if constexpr (V == 4) A(KERNEL, 1024, 8);                                                                 \
     } while (0)
     if (p.da) SHAPES(act_grad_kernel);
     else if (p.codes) SHAPES(act_int8_kernel);

@@ -10,13 +10,15 @@
 // instruction where the matrix cores have nothing else to do. fp16 parts are scaled by a
 // power of two per token, as v may lie outside fp16's range.
 //
-// Matrix operands come straight from memory: a lane holds 8 consecutive elements of one
-// row (16x16x32, rows lane % 16); any order of the depth serves as long as both operands
-// have the same, so a lane takes 16 consecutive ones for two instructions, and the four
-// lanes of a row read one line.
+// A lane's part of a matrix operand is 8 consecutive elements of row lane % 16, so 16
+// neighbouring lanes read 16 rows: straight from memory that costs the address units about
+// 50 cycles a load instead of 16, which is what bounds the narrow kernels, for few tokens an
+// adapter, where nothing but latency counts. The wide ones go through the LDS, filled by
+// direct loads of whole lines, and end with whole lines of base and out.
 #include <algorithm>
 
 #include "moe_args.h"
+#include "moe_lds_dev.h"
 #include "moe_rows_dev.h"
 #include "moe_tiles_dev.h"
 
@@ -58,9 +60,9 @@ struct AdaptArgs {
 constexpr int kStep = 64;  // depth of two matrix instructions
 
 // v of the tile's rows, NT * 16 ranks, over one part of the depth. WK of the block's four
-// waves share it among them, the others have rows of their own.
-template <typename T, int MS, int NT, int WK>
-__global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p, int most) {
+// waves share it among them, the others have rows of their own. P steps are on their way.
+template <typename T, int MS, int NT, int WK, int P>
+__global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p) {
     constexpr int WM = 4 / WK, BM = WM * MS * 16;
     __shared__ f32x4 s_acc[WK > 1 ? WK : 1][WK > 1 ? MS * NT : 1][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -75,33 +77,53 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p, int most) 
     for (int m = 0; m < MS; ++m) {
         // (rows behind the last one and entries that name no token: any token, not used)
         const int row = row0 + min(wm * MS * 16 + m * 16 + c, rows - 1), t = p.row_to_token[row];
-        xr[m] = (const T*)p.x + (int64_t)((uint32_t)t < (uint32_t)p.T ? t : 0) * p.ld_x + 16 * q;
+        xr[m] = (const T*)p.x + (int64_t)((uint32_t)t < (uint32_t)p.T ? t : 0) * p.ld_x + 8 * q;
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-        ar[j] = (const T*)p.a + e * p.a_adapter + (int64_t)min(r0 + j * 16 + c, p.r - 1) * p.ld_a + 16 * q;
+        ar[j] = (const T*)p.a + e * p.a_adapter + (int64_t)min(r0 + j * 16 + c, p.r - 1) * p.ld_a + 8 * q;
     f32x4 acc[MS][NT] = {};
     const int steps = (p.H + kStep - 1) / kStep, each = (steps + p.splits - 1) / p.splits;
-    const int hi = min(steps, (split + 1) * each);
-    for (int s = split * each + wk; s < hi; s += WK) {
+    const int lo = split * each + wk, hi = min(steps, (split + 1) * each);
+    Vec<T> xv[P][MS][2], av[P][NT][2];
+    auto load = [&](int u, int s) INLINE {
         const int k = s * kStep;
-        Vec<T> xv[MS][2] = {}, av[NT][2] = {};
-        if (k + 16 * q < p.H) {  // (H is a multiple of 16)
+        if (s >= hi) return;
+        if (k + kStep <= p.H) {
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) xv[u][m][h] = load_vec(xr[m] + k + 32 * h);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) av[j][h] = load_vec(ar[j] + k + 8 * h);
+                for (int h = 0; h < 2; ++h) av[u][j][h] = load_vec(ar[j] + k + 32 * h);
+        } else {
+            const bool in[2] = {k + 8 * q < p.H, k + 32 + 8 * q < p.H};  // (H is a multiple of 16)
 #pragma unroll
             for (int m = 0; m < MS; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) xv[m][h] = load_vec(xr[m] + k + 8 * h);
+                for (int h = 0; h < 2; ++h) xv[u][m][h] = in[h] ? load_vec(xr[m] + k + 32 * h) : Vec<T>{};
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) av[u][j][h] = in[h] ? load_vec(ar[j] + k + 32 * h) : Vec<T>{};
         }
+    };
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+    for (int u = 0; u < P; ++u) load(u, lo + u * WK);
+    for (int s = lo; s < hi; s += P * WK) {
 #pragma unroll
-            for (int m = 0; m < MS; ++m)
+        for (int u = 0; u < P; ++u) {
+            if (s + u * WK >= hi) break;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) acc[m][j] = mma(av[j][h], xv[m][h], acc[m][j]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < MS; ++m)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[m][j] = mma(av[u][j][h], xv[u][m][h], acc[m][j]);
+            load(u, s + (u + P) * WK);
+        }
     }
     // acc[m][j]: token m * 16 + c, ranks j * 16 + 4 q + 0..3
     float* part = p.part + (int64_t)split * p.T * p.r;
@@ -127,49 +149,88 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p, int most) 
     }
 }
 
-// out = base + scale b v: MS * 16 rows by 256 columns per block, 64 columns per wave. A lane ends
-// up with 16 consecutive columns of a row: the rows of b that it multiplies are dealt so.
-// Blocks behind the tiles copy the rows of tokens without an adapter.
+// out = base + scale b v: MS * 16 rows per block, 256 columns at a time (64 per wave), `chunks`
+// times, with the next columns' b and base on their way. A lane ends up with twice 8
+// consecutive columns of a row: the rows of b that it multiplies are dealt so.
+// KS: b's rows are at most 32 KS long and wait in registers (0: any length, read as
+// needed). Blocks behind the tiles copy the rows of tokens without an adapter.
 constexpr int kCopyTokens = 16;
 
-template <typename T, int MS>
-__global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, int nblocks) {
-    constexpr int BM = MS * 16;
+// The copy of one group of tokens.
+template <typename T>
+__device__ __forceinline__ void copy_tokens(const AdaptArgs& p, int group) {
+    const int tid = threadIdx.x, lane = tid & 63, t0 = group * kCopyTokens, t = t0 + (lane & 15);
+    uint32_t none = (uint32_t)__ballot(lane < kCopyTokens && t < p.T && (uint32_t)p.token_to_row[min(t, p.T - 1)] >= (uint32_t)p.T);
+    for (; none; none &= none - 1) {
+        const int64_t u = t0 + __ffs(none) - 1;
+        const T* src = (const T*)p.base + u * p.ld_base;
+        T* dst = (T*)p.out + u * p.ld_out;
+        for (int n = tid * 8; n < p.N; n += 256 * 8) {
+            if (n + 8 <= p.N) store_vec<false>(dst + n, load_vec(src + n));
+            else
+                for (int i = n; i < p.N; ++i) dst[i] = src[i];
+        }
+    }
+}
+
+// fp16: the power of two that brings a row's largest |v| (its bits) to [2^12, 2^13). (0,
+// infinity, NaN: as they are)
+__device__ __forceinline__ int power_for(uint32_t top) { return top && top < 0x7F800000u ? 12 - ilogbf(u2f(top)) : 0; }
+
+// f as hi + lo of type T (an infinity or a NaN in hi alone)
+template <typename T>
+__device__ __forceinline__ void split_value(float f, T* hi, T* lo) {
+    *hi = from_f32<T>(f);
+    const float h = to_f32(*hi);
+    *lo = from_f32<T>(fabsf(h) < __builtin_huge_valf() ? f - h : 0.0f);
+}
+
+template <typename T, int MS, int KS>
+__global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, int nblocks, int chunks) {
+    constexpr int BM = MS * 16, KR = KS ? KS : 1;
     extern __shared__ __align__(16) char s_room[];
     __shared__ float s_back[BM];  // what undoes the tokens' powers of two, times the adapter's scale
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
     const int tile = blockIdx.x / nblocks;
     if (tile >= most) {
-        const int t0 = (blockIdx.x - most * nblocks) * kCopyTokens, t = t0 + c;
-        uint32_t none = (uint32_t)__ballot(lane < kCopyTokens && t < p.T && (uint32_t)p.token_to_row[min(t, p.T - 1)] >= (uint32_t)p.T);
-        for (; none; none &= none - 1) {
-            const int64_t u = t0 + __ffs(none) - 1;
-            const T* src = (const T*)p.base + u * p.ld_base;
-            T* dst = (T*)p.out + u * p.ld_out;
-            for (int n = tid * 8; n < p.N; n += 256 * 8) {
-                if (n + 8 <= p.N) store_vec<false>(dst + n, load_vec(src + n));
-                else
-                    for (int i = n; i < p.N; ++i) dst[i] = src[i];
-            }
-        }
+        copy_tokens<T>(p, blockIdx.x - most * nblocks);
         return;
     }
     int e, row0, rows;
     if (!find_tile<BM>(p.offsets, p.n, p.T, tile, lane, &e, &row0, &rows)) return;
-    const int n0 = (blockIdx.x % nblocks) * 256 + wave * 64, n = n0 + 16 * q;
-    int token[MS];
-    Vec<T> base[MS][2];
+    int64_t token[MS];
 #pragma unroll
     for (int m = 0; m < MS; ++m) {
         const int row = m * 16 + c, t = row < rows ? p.row_to_token[row0 + row] : -1;
         token[m] = (uint32_t)t < (uint32_t)p.T ? t : -1;
-        if (token[m] >= 0 && n + 16 <= p.N) {
-            base[m][0] = load_vec((const T*)p.base + token[m] * p.ld_base + n);
-            base[m][1] = load_vec((const T*)p.base + token[m] * p.ld_base + n + 8);
-        }
     }
+    const int first = (blockIdx.x % nblocks) * chunks * 256 + wave * 64;
+    const T* b = (const T*)p.b + e * p.b_adapter;
+    Vec<T> base[MS][2], bv[KR][4];
+    auto load_base = [&](int n0) INLINE {
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int n = n0 + 32 * g + 8 * q;
+                if (token[m] >= 0 && n + 8 <= p.N) base[m][g] = load_vec((const T*)p.base + token[m] * p.ld_base + n);
+            }
+    };
+    auto load_b = [&](int n0, int k, Vec<T>* v) INLINE {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            v[u] = Vec<T>{};
+            // row 4 i + j of instruction u is column 32 (u / 2) + 8 i + 4 (u % 2) + j (r is a multiple of 8)
+            if (k < p.r) v[u] = load_vec(b + (int64_t)min(n0 + 32 * (u >> 1) + 8 * (c >> 2) + 4 * (u & 1) + (c & 3), p.N - 1) * p.ld_b + k);
+        }
+    };
+    if (KS) {
+#pragma unroll
+        for (int s = 0; s < KR; ++s) load_b(first, 32 * s + 8 * q, bv[s]);
+    }
+    load_base(first);
     // v: fp32 [BM][wide], then its parts hi and lo [BM][wide] each
-    const int deep = (p.r + 31) / 32 * 32, wide = deep + 8;
+    const int deep = KS ? 32 * KS : (p.r + 31) / 32 * 32, wide = deep + 8;
     float* v = (float*)s_room;
     T *v_hi = (T*)(v + BM * wide), *v_lo = v_hi + BM * wide;
     {
@@ -180,69 +241,348 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
             f32x4 sum = {};
             if (row < rows && j < p.r) {
                 const float* src = p.part + (int64_t)(row0 + row) * p.r + j;
-                for (int s = 0; s < p.splits; ++s) sum += *reinterpret_cast<const f32x4*>(src + (int64_t)s * p.T * p.r);
+                const int64_t far = (int64_t)p.T * p.r;
+                for (int s = 0; s < p.splits; s += 8) {  // eight loads on their way, added in order
+                    f32x4 w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const f32x4*>(src + min(s + i, p.splits - 1) * far);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum += s + i < p.splits ? w[i] : f32x4{};
+                }
             }
             *reinterpret_cast<f32x4*>(v + row * wide + j) = sum;
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = max(top, f2u(sum[i]) & 0x7FFFFFFFu);
         }
-        // fp16: the largest |v| of the row to [2^12, 2^13). (0, infinity, NaN: as they are)
         int up = 0;
         if constexpr (std::is_same<T, Fp16>::value) {
 #pragma unroll
             for (int off = TPR / 2; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-            if (top && top < 0x7F800000u) up = 12 - (ilogbf(u2f(top)));
+            up = power_for(top);
         }
         if (at == 0) s_back[row] = ldexpf(p.scales ? p.scales[e] : 1.0f, -up);
         for (int j = at * 4; j < deep; j += TPR * 4)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float f = ldexpf(v[row * wide + j + i], up);
-                const T h = from_f32<T>(f);
-                const float rest = f - to_f32(h);
-                v_hi[row * wide + j + i] = h;
-                v_lo[row * wide + j + i] = from_f32<T>(fabsf(to_f32(h)) < __builtin_huge_valf() ? rest : 0.0f);
-            }
+            for (int i = 0; i < 4; ++i)
+                split_value(ldexpf(v[row * wide + j + i], up), &v_hi[row * wide + j + i], &v_lo[row * wide + j + i]);
     }
     __syncthreads();
-    if (n0 >= p.N) return;
-    f32x4 acc[MS][4] = {};
-    const T* b = (const T*)p.b + e * p.b_adapter;
-    for (int k = 8 * q; k < deep; k += 32) {
-        Vec<T> bv[4] = {};
-        if (k < p.r) {  // (r is a multiple of 8)
+    for (int i = 0; i < chunks; ++i) {
+        const int n0 = first + i * 256;
+        if (n0 >= p.N) return;
+        const bool more = i + 1 < chunks && n0 + 256 < p.N;
+        f32x4 acc[MS][4] = {};
+        auto multiply = [&](int k, const Vec<T>* w) INLINE {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)  // row i = 4 (c / 4) + c % 4 of instruction u is column 16 (c / 4) + 4 u + c % 4
-                bv[u] = load_vec(b + (int64_t)min(n0 + 16 * (c >> 2) + 4 * u + (c & 3), p.N - 1) * p.ld_b + k);
-        }
+            for (int m = 0; m < MS; ++m) {
+                const Vec<T> hi = *reinterpret_cast<const Vec<T>*>(v_hi + (m * 16 + c) * wide + k);
+                const Vec<T> lo = *reinterpret_cast<const Vec<T>*>(v_lo + (m * 16 + c) * wide + k);
 #pragma unroll
-        for (int m = 0; m < MS; ++m) {
-            const Vec<T> hi = *reinterpret_cast<const Vec<T>*>(v_hi + (m * 16 + c) * wide + k);
-            const Vec<T> lo = *reinterpret_cast<const Vec<T>*>(v_lo + (m * 16 + c) * wide + k);
+                for (int u = 0; u < 4; ++u) acc[m][u] = mma(w[u], hi, mma(w[u], lo, acc[m][u]));
+            }
+        };
+        if constexpr (KS > 0) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[m][u] = mma(bv[u], hi, mma(bv[u], lo, acc[m][u]));
-        }
-    }
-    // acc[m][u]: token m * 16 + c, columns n + 4 u + 0..3
+            for (int s = 0; s < KS; ++s) multiply(32 * s + 8 * q, bv[s]);
+            if (more) {
 #pragma unroll
-    for (int m = 0; m < MS; ++m) {
-        if (token[m] < 0) continue;
-        const float back = s_back[m * 16 + c];
-        T* dst = (T*)p.out + token[m] * p.ld_out + n;
-        if (n + 16 <= p.N) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                Vec<T> o;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o.e[i] = from_f32<T>(__fmaf_rn(acc[m][2 * g + i / 4][i % 4], back, to_f32(base[m][g].e[i])));
-                store_vec<false>(dst + 8 * g, o);
+                for (int s = 0; s < KS; ++s) load_b(n0 + 256, 32 * s + 8 * q, bv[s]);
             }
         } else {
-            const T* src = (const T*)p.base + token[m] * p.ld_base + n;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (n + i < p.N) dst[i] = from_f32<T>(__fmaf_rn(acc[m][i / 4][i % 4], back, to_f32(src[i])));
+            for (int k = 8 * q; k < deep; k += 32) {
+                load_b(n0, k, bv[0]);
+                multiply(k, bv[0]);
+            }
         }
+        // acc[m][u]: token m * 16 + c, columns n0 + 32 (u / 2) + 8 q + 4 (u % 2) + 0..3
+#pragma unroll
+        for (int m = 0; m < MS; ++m) {
+            if (token[m] < 0) continue;
+            const float back = s_back[m * 16 + c];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int n = n0 + 32 * g + 8 * q;
+                T* dst = (T*)p.out + token[m] * p.ld_out + n;
+                if (n + 8 <= p.N) {
+                    Vec<T> o;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o.e[j] = from_f32<T>(__fmaf_rn(acc[m][2 * g + j / 4][j % 4], back, to_f32(base[m][g].e[j])));
+                    store_vec<false>(dst, o);
+                } else {
+                    const T* src = (const T*)p.base + token[m] * p.ld_base + n;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n + j < p.N) dst[j] = from_f32<T>(__fmaf_rn(acc[m][2 * g + j / 4][j % 4], back, to_f32(src[j])));
+                }
+            }
+        }
+        if (more) load_base(n0 + 256);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// many tokens an adapter
+// ---------------------------------------------------------------------------
+// v of 64 * MS rows, 16 * MS a wave, NT * 16 ranks, over one part of the depth: steps of 128
+// bytes of depth through P LDS buffers. The wave's own rows of x and its share of those of
+// a: one load brings 8 rows of 128 bytes, chunk (l % 8) ^ mix(row) of row l / 8 to lane l, so
+// that an operand read (one chunk of 16 rows) uses all banks.
+template <typename T, int MS, int NT, int P>
+__global__ __launch_bounds__(256) void adapt_down_wide_kernel(AdaptArgs p, uint32_t x_bytes) {
+    constexpr int LX = 2 * MS, LA = NT > 2 ? NT / 2 : 1, L = LX + LA, kRow = 128, kRows = 64 * MS;
+    constexpr int kA = kRows * kRow, BUF = kA + 4 * LA * 8 * kRow;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[P * BUF];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+    const int split = blockIdx.x % p.splits;
+    int e, row0, rows;
+    if (!find_tile<kRows>(p.offsets, p.n, p.T, blockIdx.x / p.splits, lane, &e, &row0, &rows)) return;
+    const int r0 = blockIdx.y * NT * 16;
+    auto mix = [](int row) INLINE { return (row >> 1) & 7; };
+    // (rows behind the last one and entries that name no token: any token, not used)
+    uint32_t xo[LX], ao[LA];  // where a lane's rows begin
+    int xk[LX], ak[LA];       // where its chunk begins in a step
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+        const int row = (wave * LX + i) * 8 + (lane >> 3), t = p.row_to_token[row0 + min(row, rows - 1)];
+        xk[i] = ((lane & 7) ^ mix(row)) * 8;
+        xo[i] = ((uint32_t)t < (uint32_t)p.T ? t : 0) * (uint32_t)(p.ld_x * 2) + xk[i] * 2;
+    }
+    const T* a = (const T*)p.a + e * p.a_adapter + r0 * p.ld_a;
+    const int ranks = min(NT * 16, p.r - r0);
+    const uint32_t a_bytes = (uint32_t)((ranks - 1) * p.ld_a + p.H) * 2;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const int row = (wave + 4 * i) * 8 + (lane >> 3);
+        ak[i] = ((lane & 7) ^ mix(row)) * 8;
+        ao[i] = (uint32_t)min(row, ranks - 1) * (uint32_t)(p.ld_a * 2) + ak[i] * 2;
+    }
+    const int steps = (p.H + kStep - 1) / kStep, each = (steps + p.splits - 1) / p.splits;
+    const int lo = split * each, hi = min(steps, lo + each);
+    // (always L loads: those of steps behind the last bring zeros that nothing reads)
+    auto issue = [&](int s, int buf) INLINE {
+        const int k = s * kStep, left = s < hi ? p.H - k : 0;
+        uint8_t* at = lds + buf * BUF;
+        if (left >= kStep) {
+#pragma unroll
+            for (int i = 0; i < LX; ++i) buffer_load_lds16<false>(p.x, x_bytes, xo[i] + k * 2, at + (wave * LX + i) * 8 * kRow);
+#pragma unroll
+            for (int i = 0; i < LA; ++i) buffer_load_lds16<false>(a, a_bytes, ao[i] + k * 2, at + kA + (wave + 4 * i) * 8 * kRow);
+        } else {
+#pragma unroll
+            for (int i = 0; i < LX; ++i)
+                buffer_load_lds16<false>(p.x, x_bytes, xk[i] < left ? xo[i] + k * 2 : kOutOfRange, at + (wave * LX + i) * 8 * kRow);
+#pragma unroll
+            for (int i = 0; i < LA; ++i)
+                buffer_load_lds16<false>(a, a_bytes, ak[i] < left ? ao[i] + k * 2 : kOutOfRange, at + kA + (wave + 4 * i) * 8 * kRow);
+        }
+    };
+    f32x4 acc[MS][NT] = {};
+#pragma unroll
+    for (int u = 0; u < P - 1; ++u) issue(lo + u, u);
+    const uint32_t base = lds_address(lds) + c * kRow;
+    int buf = 0, next = P - 1;
+    for (int s = lo; s < hi; ++s) {
+        wait_and_barrier<L*(P - 2)>();
+        issue(s + P - 1, next);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = base + buf * BUF + (((4 * h + q) ^ mix(c)) << 4);
+            uint32_t from[MS + NT];
+            u32x4 v[MS + NT];
+#pragma unroll
+            for (int m = 0; m < MS; ++m) from[m] = at + (wave * MS + m) * 16 * kRow;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) from[MS + j] = at + kA + j * 16 * kRow;
+            lds_read(v, from);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int m = 0; m < MS; ++m)
+                    acc[m][j] = mma(__builtin_bit_cast(Vec<T>, v[MS + j]), __builtin_bit_cast(Vec<T>, v[m]), acc[m][j]);
+        }
+        buf = buf + 1 == P ? 0 : buf + 1;
+        next = next + 1 == P ? 0 : next + 1;
+    }
+    // acc[m][j]: token m * 16 + c, ranks j * 16 + 4 q + 0..3
+    float* part = p.part + (int64_t)split * p.T * p.r;
+#pragma unroll
+    for (int m = 0; m < MS; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int row = (wave * MS + m) * 16 + c, rank = r0 + j * 16 + 4 * q;
+            if (row < rows && rank < p.r) *reinterpret_cast<f32x4*>(part + (int64_t)(row0 + row) * p.r + rank) = acc[m][j];
+        }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into the LDS outlives the block
+}
+
+// out = base + scale b v for 4 * MS * 16 rows, 128 columns at a time, `chunks` times. The block's
+// waves share the columns' rows of b in the LDS (two buffers) and have rows of their own,
+// whose v waits in registers. Lane (c, q) holds columns 8 c .. 8 c + 7 of tokens 4 q .. 4 q + 3:
+// row 8 c + u of b is column c of instruction u and lies in row 16 u + c of the buffer, its
+// chunks mixed (where their number is a power of two) so that 16 rows use all banks.
+template <typename T, int MS, int KS>
+__global__ __launch_bounds__(256) void adapt_up_wide_kernel(AdaptArgs p, int most, int nblocks, int chunks) {
+    constexpr int BM = 64 * MS, kColumns = 128;
+    extern __shared__ __align__(1024) char s_room[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+    const int tile = blockIdx.x / nblocks;
+    if (tile >= most) {
+        copy_tokens<T>(p, blockIdx.x - most * nblocks);
+        return;
+    }
+    int e, row0, rows;
+    if (!find_tile<BM>(p.offsets, p.n, p.T, tile, lane, &e, &row0, &rows)) return;
+    const int first = (blockIdx.x % nblocks) * chunks * kColumns;
+    const int rc = p.r / 8, pitch = p.r * 2, size = kColumns * pitch;
+    // 2^shift chunks of 16 bytes: a row of 16 (c) lies 128 bytes behind the row 8 / chunks before it
+    const int shift = rc & (rc - 1) ? -1 : __builtin_ctz(rc);
+    auto mix = [&](int row) INLINE { return shift < 0 ? 0 : shift >= 3 ? (row >> 1) & 7 : (row >> (4 - shift)) & ((1 << shift) - 1); };
+    const T* b = (const T*)p.b + e * p.b_adapter;
+    auto issue = [&](int n0, int buf) INLINE {
+        for (int i = wave; i < 2 * rc; i += 4) {
+            const int slot = i * 64 + lane, at = slot / rc, chunk = (slot - at * rc) ^ mix(at & 15);
+            const int n = min(8 * (at & 15) + (at >> 4), p.N - 1 - n0);
+            buffer_load_lds16<false>(b + n0 * p.ld_b, 128u * (uint32_t)(p.ld_b * 2), (uint32_t)n * (uint32_t)(p.ld_b * 2) + chunk * 16,
+                                     s_room + buf * size + i * 1024);
+        }
+    };
+    const uint32_t room = lds_address(s_room);
+    issue(first, 0);
+    // v of the wave's rows (those behind the last are the last one's again)
+    Vec<T> hi[MS][KS], lo[MS][KS];
+    float back[MS][4];
+    int token[MS][4];
+#pragma unroll
+    for (int m = 0; m < MS; ++m) {
+        const int row = row0 + min((wave * MS + m) * 16 + c, rows - 1);
+        const int t = p.row_to_token[row], named = (uint32_t)t < (uint32_t)p.T && (wave * MS + m) * 16 + c < rows ? t : -1;
+        float f[KS][8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int k = 32 * s + 8 * q;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[s][i] = 0.0f;
+            if (k < p.r) {
+                const float* src = p.part + (int64_t)row * p.r + k;
+                for (int z = 0; z < p.splits; ++z, src += (int64_t)p.T * p.r) {
+                    const f32x4 u = *reinterpret_cast<const f32x4*>(src), w = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[s][i] += u[i], f[s][4 + i] += w[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, f2u(f[s][i]) & 0x7FFFFFFFu);
+        }
+        int up = 0;
+        if constexpr (std::is_same<T, Fp16>::value) {
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+            up = power_for(top);
+        }
+        const float undo = ldexpf(p.scales ? p.scales[e] : 1.0f, -up);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            back[m][i] = __shfl(undo, 4 * q + i);
+            token[m][i] = __shfl(named, 4 * q + i);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split_value(ldexpf(f[s][i], up), &hi[m][s].e[i], &lo[m][s].e[i]);
+    }
+    // Base of a pass, always MS * 4 loads (none where a row has no 8 columns: then there is one
+    // pass), so that the wait below can count them.
+    typedef u32x4 Base[MS][4];
+    auto load_base = [&](int n0, Base& base) INLINE {
+        if (p.N < 8) return;
+        const int n = min(n0 + 8 * c, p.N - 8);
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) base[m][i] = __builtin_bit_cast(u32x4, load_vec((const T*)p.base + max(token[m][i], 0) * p.ld_base + n));
+    };
+    // Makes the compiler wait for these loads here, and not where the values are used.
+    auto have = [](Base& base) INLINE {
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(base[m][i]));
+    };
+    bool named = true;  // all rows of the wave
+#pragma unroll
+    for (int m = 0; m < MS; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) named &= token[m][i] >= 0;
+    named = __ballot(!named) == 0;
+    const int end = min(first + chunks * kColumns, p.N);
+    auto pass = [&](int n0, int buf, Base& base, Base& next) INLINE {
+        have(base);
+        if (n0 + kColumns < end) {
+            issue(n0 + kColumns, buf ^ 1);
+            load_base(n0 + kColumns, next);
+        }
+        f32x4 acc[MS][8] = {};
+        const uint32_t rows_of_b = room + buf * size + c * pitch;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int k = 4 * s + q;  // chunk
+            uint32_t from[8];
+            u32x4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) from[u] = rows_of_b + 16 * u * pitch + ((min(k, rc - 1) ^ mix(c)) << 4);
+            lds_read(v, from);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (p.r % 32 && k >= rc) v[u] = u32x4{};
+                const Vec<T> bv = __builtin_bit_cast(Vec<T>, v[u]);
+#pragma unroll
+                for (int m = 0; m < MS; ++m) acc[m][u] = mma(hi[m][s], bv, mma(lo[m][s], bv, acc[m][u]));
+            }
+        }
+        const int n = n0 + 8 * c;
+        auto result = [&](int m, int i) INLINE {
+            const Vec<T> old = __builtin_bit_cast(Vec<T>, base[m][i]);
+            Vec<T> o;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o.e[u] = from_f32<T>(__fmaf_rn(acc[m][u][i], back[m][i], to_f32(old.e[u])));
+            return o;
+        };
+        if (named && n0 + kColumns <= p.N) {
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) store_vec<false>((T*)p.out + token[m][i] * p.ld_out + n, result(m, i));
+            return;
+        }
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (token[m][i] < 0) continue;
+                T* dst = (T*)p.out + token[m][i] * p.ld_out + n;
+                if (n + 8 <= p.N) {
+                    store_vec<false>(dst, result(m, i));
+                } else {
+                    const T* src = (const T*)p.base + token[m][i] * p.ld_base + n;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (n + u < p.N) dst[u] = from_f32<T>(__fmaf_rn(acc[m][u][i], back[m][i], to_f32(src[u])));
+                }
+            }
+        have(next);
+    };
+    Base one, two;
+    load_base(first, one);
+    wait_and_barrier<0>();
+    for (int n0 = first; n0 < end; n0 += 2 * kColumns) {
+        pass(n0, 0, one, two);
+        if (n0 + kColumns >= end) break;
+        // the next columns' rows of b have landed once no more than MS * 4 operations are left: behind
+        // them came as many loads of base, and whatever stores
+        wait_and_barrier<MS * 4>();
+        pass(n0 + kColumns, 1, two, one);
+        if (n0 + 2 * kColumns < end) wait_and_barrier<MS * 4>();
     }
 }
 
@@ -254,48 +594,80 @@ constexpr int kMaxRank = 256, kMaxSplits = 16;
 // Tiles of bm rows there can be: whole ones, and a last one for each adapter with rows.
 static int64_t most_tiles(int T, int n, int bm) { return T / bm + std::min(n, T); }
 
+constexpr int kWideRows = 128;  // of a tile of the first product
+
 struct AdaptPlan {
-    bool wide;  // 128-row tiles in the first product, 64-row ones in the second
+    bool wide;  // the kernels for many tokens an adapter
     int splits;
 };
 static AdaptPlan plan_adapt(int T, int n, int H) {
     AdaptPlan q;
     q.wide = T >= 64 * (int64_t)std::min(n, T);
-    const int64_t tiles = q.wide ? T / 128 + 1 : most_tiles(T, n, 16);
+    const int64_t tiles = q.wide ? T / kWideRows + 1 : most_tiles(T, n, 16);
     const int64_t most = std::max((H + kStep * 4 - 1) / (kStep * 4), 1);
     q.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, most, kMaxSplits}));
     return q;
 }
 
-template <typename T, int MS, int WK>
-static void launch_down(const AdaptArgs& p, hipStream_t s) {
-    const int most = (int)most_tiles(p.T, p.n, 4 / WK * MS * 16);
-#define D(NT)                                                                                                         \
-    hipLaunchKernelGGL((adapt_down_kernel<T, MS, NT, WK>), dim3(most * p.splits, (p.r + NT * 16 - 1) / (NT * 16)),     \
-                       dim3(256), 0, s, p, most)
-    if (p.r <= 16) D(1);
-    else if (p.r <= 32) D(2);
-    else D(4);
+// Bytes from the first token's row to the last one's end.
+static int64_t x_extent(const AdaptArgs& p) { return ((p.T - 1) * p.ld_x + p.H) * 2; }
+
+template <typename T>
+static void launch_down(const AdaptArgs& p, bool wide, hipStream_t s) {
+    const int most = (int)most_tiles(p.T, p.n, wide ? kWideRows : 16);
+#define D(KERNEL, NT)                                                                                                  \
+    hipLaunchKernelGGL(KERNEL, dim3(most * p.splits, (p.r + NT * 16 - 1) / (NT * 16)), dim3(256), 0, s, MORE)
+    if (wide) {
+#define MORE p, (uint32_t)x_extent(p)
+        constexpr int MS = kWideRows / 64;
+        if (p.r <= 16) D((adapt_down_wide_kernel<T, MS, 1, 3>), 1);
+        else if (p.r <= 32) D((adapt_down_wide_kernel<T, MS, 2, 3>), 2);
+        else D((adapt_down_wide_kernel<T, MS, 4, 3>), 4);
+#undef MORE
+    } else {
+#define MORE p
+        if (p.r <= 16) D((adapt_down_kernel<T, 1, 1, 4, 3>), 1);
+        else if (p.r <= 32) D((adapt_down_kernel<T, 1, 2, 4, 3>), 2);
+        else D((adapt_down_kernel<T, 1, 4, 4, 3>), 4);
+#undef MORE
+    }
 #undef D
 }
 
-template <typename T, int MS>
-static void launch_up(const AdaptArgs& p, hipStream_t s) {
-    const int most = (int)most_tiles(p.T, p.n, MS * 16), nblocks = (p.N + 255) / 256;
+template <typename T>
+static hipError_t launch_up(const AdaptArgs& p, bool wide, hipStream_t s) {
+    const int rows = wide ? 64 : 16, step = wide ? 128 : 256;
+    const int64_t most = most_tiles(p.T, p.n, rows), columns = (p.N + step - 1) / step;
+    // columns a block walks over: about 1024 blocks, no more than 8 times (wide: what is left)
+    const int chunks = (int)std::min<int64_t>(std::max<int64_t>(most * columns / 1024, 1), wide ? 16 : 8);
+    const int nblocks = (int)((columns + chunks - 1) / chunks);
     const int copy = p.out == p.base ? 0 : (p.T + kCopyTokens - 1) / kCopyTokens;
-    const int wide = (p.r + 31) / 32 * 32 + 8;
-    hipLaunchKernelGGL((adapt_up_kernel<T, MS>), dim3(most * nblocks + copy), dim3(256), MS * 16 * wide * 8, s, p, most, nblocks);
+    const int lds = wide ? 2 * 128 * p.r * 2 : 16 * ((p.r + 31) / 32 * 32 + 8) * 8;
+#define U(KERNEL)                                                                                                      \
+    hipLaunchKernelGGL((KERNEL), dim3((int)most * nblocks + copy), dim3(256), lds, s, p, (int)most, nblocks, chunks)
+    if (wide) {
+        if (p.r <= 32) U((adapt_up_wide_kernel<T, 1, 1>));
+        else if (p.r <= 64) U((adapt_up_wide_kernel<T, 1, 2>));
+        else if (p.r <= 128) U((adapt_up_wide_kernel<T, 1, 4>));
+        else U((adapt_up_wide_kernel<T, 1, 8>));
+    } else {
+        if (p.r <= 32) U((adapt_up_kernel<T, 1, 1>));
+        else if (p.r <= 64) U((adapt_up_kernel<T, 1, 2>));
+        else U((adapt_up_kernel<T, 1, 0>));
+    }
+#undef U
+    return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t launch_adapt(AdaptArgs p, hipStream_t s) {
     const AdaptPlan q = plan_adapt(p.T, p.n, p.H);
     p.splits = q.splits;
-    if (q.wide) launch_down<T, 2, 1>(p, s);
-    else launch_down<T, 1, 4>(p, s);
-    if (q.wide && p.r <= 96) launch_up<T, 4>(p, s);
-    else launch_up<T, 1>(p, s);
-    return hipGetLastError();
+    // (the wide kernels address the rows of x, 64 of a and 128 of b by 32-bit offsets; the
+    // workspace fits either)
+    const bool wide = q.wide && x_extent(p) <= (int64_t)kOutOfRange && p.ld_a <= (1 << 24) && p.ld_b <= (1 << 23);
+    launch_down<T>(p, wide, s);
+    return launch_up<T>(p, wide, s);
 }
 
 static int check_adapt_sizes(int T, int n, int H, int r, int N) {

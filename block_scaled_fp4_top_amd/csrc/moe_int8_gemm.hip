@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "moe_args.h"
+#include "moe_lds_dev.h"
 #include "moe_rows_dev.h"
 #include "moe_tiles_dev.h"
 
@@ -102,32 +103,10 @@ struct __attribute__((packed, aligned(sizeof(T)))) Few {
     T e[N];
 };
 
-// Direct buffer -> LDS load of 16 bytes per lane from `base` + `off` (zeros from
-// `bytes` on): lane l's bytes land at dst + 16 l (dst is uniform across the wave).
-// ONCE: a non-temporal load, for lines that are read once: the rows of B of an
-// expert with one M-tile. 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us then;
+// buffer_load_lds16's ONCE is for the rows of B of an expert with one M-tile. 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us then;
 // mean rows of 16, 48, 64, 128 over 128 experts of 4096 x 4096 359 -> 325, 406 -> 377,
 // 422 -> 404, 516 -> 504 (with all of B non-temporal 326, 391, 443, 540: experts with
 // several tiles then lose their L2).
-template <bool ONCE>
-__device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t bytes, uint32_t off, void* dst) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000),
-                                             (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, ONCE ? 2 : 0);
-}
-
-// s_waitcnt until no vector-memory and no LDS operation of this wave is
-// outstanding, then the workgroup barrier.
-template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// The workgroup barrier once this wave's LDS operations are done (loads into the
-// LDS may still be on their way).
-__device__ __forceinline__ void wait_lds_and_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // Stores N consecutive results of one row past the caches (nothing reads them here
 // again; with normal stores they push rows of A and B out of the L2: 16384 x 4096 x
 // 7168 went from 454 to 437 us, 98304 x 2048 x 2048 in 64 groups from 525 to 482).
@@ -148,10 +127,6 @@ __device__ __forceinline__ void store_past_caches(T* dst, const Few<T, N>& v) {
 
 // Until this wave's loads (and stores) are done.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// Byte offset that lies behind every buffer (their extents are checked on the
-// host to be at most this): loads there return zeros.
-constexpr uint32_t kOutOfRange = 0xFFFF0000u;
 
 // One block per CU walks tiles of BM x BN (BM rows of one expert); NW = WM * WN
 // waves of ME * 16 rows x NT * 16 columns each (row group g of the tile belongs to

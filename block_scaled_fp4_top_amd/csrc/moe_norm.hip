@@ -359,8 +359,8 @@ static hipError_t launch_norm(const NormArgs<T, W>& p, hipStream_t s) {
     else if (vecs <= 256) N(256, 1);
     else if (vecs <= 512) N(256, 2);
     else if (vecs <= 1024) N(256, 4);
-    else if (vecs <= 4096) N(1024, 4);
-    else N(1024, 8);
+    else if (V == 8 || vecs <= 4096) N(1024, 4);
+    else if constexpr (V == 4) N(1024, 8);
 #undef N
     return hipGetLastError();
 }
@@ -376,8 +376,8 @@ static hipError_t launch_norm_grad(const NormGradArgs<T, W>& p, float* dweight, 
     else if (vecs <= 512) N(256, 2);
     else if (vecs <= 1024) N(512, 2);
     else if (vecs <= 2048) N(1024, 2);
-    else if (vecs <= 4096) N(1024, 4);
-    else N(1024, 8);
+    else if (V == 8 || vecs <= 4096) N(1024, 4);
+    else if constexpr (V == 4) N(1024, 8);
 #undef N
     if (dweight)
         hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((p.H + 63) / 64), dim3(256), 0, s, p.part, blocks, p.H, dweight);

@@ -488,7 +488,8 @@ def test_activate_grad_against_differences():
 #          T, n, r, H, N
 ADAPTS = [(1, 1, 8, 16, 1), (1, 8, 16, 7168, 4096), (3, 2, 8, 48, 17), (64, 32, 16, 1024, 520), (17, 1024, 8, 64, 100),
           (70, 3, 40, 208, 300), (33, 4, 256, 320, 257), (200, 2, 64, 512, 130), (500, 3, 72, 144, 70), (300, 1, 16, 2048, 64),
-          (129, 1, 104, 272, 96), (640, 4, 32, 96, 1000)]
+          (129, 1, 104, 272, 96), (640, 4, 32, 96, 1000), (200, 1, 256, 64, 200), (300, 2, 128, 80, 300), (260, 4, 64, 7168, 137),
+          (130, 1, 8, 400, 128)]
 
 
 def adapter_case(seed, T, n, r, H, N, dtype, none):
