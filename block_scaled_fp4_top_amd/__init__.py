@@ -675,6 +675,7 @@ def int8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
 # activation, low-rank adapters. The same conventions as above.
 # ---------------------------------------------------------------------------
 SCORES = {"softmax": 0, "sigmoid": 1}
+_ROWS = torch.contiguous_format  # (empty_like keeps the order of an expanded tensor's strides else)
 
 
 def _choice(table, key, name):
@@ -713,12 +714,11 @@ def route(logits: torch.Tensor, K: int, score: str = "softmax", bias=None, group
     b = None if bias is None else _vector(bias, "bias", dev, (E,))
     if K < 0:
         raise ValueError(f"K={K} is negative")
-    both = torch.empty((2, T, K), dtype=torch.int32, device=logits.device)
-    p = both.data_ptr()
+    ids = logits.new_empty((T, K), dtype=torch.int32)
+    weights = torch.empty_like(ids, dtype=torch.float32)
     _check(_lib.moe_route(logits.data_ptr(), ld, dt, b, T, E, K, sc, groups, top_groups, group_top,
-                          1 if renormalize else 0, scale, p, p + 4 * T * K, _raw_stream(dev)))
-    ids, weights = both.unbind(0)
-    return ids, weights.view(torch.float32)
+                          1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _raw_stream(dev)))
+    return ids, weights
 
 
 def route_grad(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
@@ -739,7 +739,7 @@ def route_grad(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, 
     dw = _vector(dweights, "dweights", dev, (T, K))
     _need(ids, "ids", torch.int32, (T, K), logits.device)
     if out is None:
-        out, ld_out = torch.empty((T, E), dtype=logits.dtype, device=logits.device), E
+        out, ld_out = torch.empty_like(logits, memory_format=_ROWS), E
     else:
         ld_out = _matrix(out, "out", logits.dtype, dev, T, E)
     _check(_lib.moe_route_grad(dw, logits.data_ptr(), ld, dt, ids.data_ptr(), T, E, K, _choice(SCORES, score, "score"),
@@ -772,7 +772,7 @@ def _norm(x, weight, eps, residual, total, y, codes, scales, dev, want_y, want_c
     if residual is not None:
         ldr, rp = _matrix(residual, "residual", x.dtype, dev, T, H), residual.data_ptr()
         if total is None:
-            total, ldt = torch.empty((T, H), dtype=x.dtype, device=x.device), H
+            total, ldt = torch.empty_like(x, memory_format=_ROWS), H
         else:
             ldt = _matrix(total, "total", x.dtype, dev, T, H)
         tp = total.data_ptr()
@@ -782,15 +782,15 @@ def _norm(x, weight, eps, residual, total, y, codes, scales, dev, want_y, want_c
     if y is not None:
         ldy, yp = _matrix(y, "y" if want_codes else "out", x.dtype, dev, T, H), y.data_ptr()
     elif want_y:
-        y, ldy = torch.empty((T, H), dtype=x.dtype, device=x.device), H
+        y, ldy = torch.empty_like(x, memory_format=_ROWS), H
         yp = y.data_ptr()
     if want_codes:
         if codes is None:
-            codes, ldc = torch.empty((T, H), dtype=torch.int8, device=x.device), H
+            codes, ldc = torch.empty_like(x, dtype=torch.int8, memory_format=_ROWS), H
         else:
             ldc = _matrix(codes, "out", torch.int8, dev, T, H)
         if scales is None:
-            scales = torch.empty(T, dtype=torch.float32, device=x.device)
+            scales = x.new_empty(T, dtype=torch.float32)
             sp = scales.data_ptr()
         else:
             sp = _vector(scales, "scales", dev, (T,))
@@ -842,7 +842,7 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight=None, eps: float = 1
     if dtotal is not None:
         ldt, tp = _matrix(dtotal, "dtotal", dy.dtype, dev, T, H), dtotal.data_ptr()
     if out is None:
-        out, ld_out = torch.empty((T, H), dtype=dy.dtype, device=dy.device), H
+        out, ld_out = torch.empty_like(dy, memory_format=_ROWS), H
     else:
         ld_out = _matrix(out, "out", dy.dtype, dev, T, H)
     dw, n, ws, dwp = None, 0, None, None
@@ -850,8 +850,8 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight=None, eps: float = 1
         n = _lib.moe_rms_norm_grad_workspace_bytes(T, H)
         if n == 0:
             raise MoeError(2, _lib.moe_last_error().decode())
-        dw = torch.empty(H, dtype=torch.float32, device=dy.device)
-        room = torch.empty(n, dtype=torch.uint8, device=dy.device)
+        dw = dy.new_empty(H, dtype=torch.float32)
+        room = dy.new_empty(n, dtype=torch.uint8)
         ws, dwp = room.data_ptr(), dw.data_ptr()
     _check(_lib.moe_rms_norm_grad(dy.data_ptr(), ld, h.data_ptr(), ldh, dt, w, wdt if w else dt, tp, ldt, T, H, eps, ws, n,
                                   out.data_ptr(), ld_out, dwp, _raw_stream(dev)))
@@ -891,7 +891,7 @@ def activate(h: torch.Tensor, act: str = "swiglu", order=None, weights=None, out
         return _elsewhere(activate, (h, act, order, weights, out), stream)
     dt, ld, code, M, I, off, E, r2r, w = _act_rows(h, act, order, weights, dev)
     if out is None:
-        out, ld_out = torch.empty((M, I), dtype=h.dtype, device=h.device), I
+        out, ld_out = h.new_empty((M, I)), I
     else:
         ld_out = _matrix(out, "out", h.dtype, dev, M, I)
     _check(_lib.moe_activate(h.data_ptr(), ld, dt, code, M, I, off, E, r2r, w, out.data_ptr(), ld_out, _raw_stream(dev)))
@@ -907,11 +907,11 @@ def activate_int8(h: torch.Tensor, act: str = "swiglu", order=None, weights=None
         return _elsewhere(activate_int8, (h, act, order, weights, out, scales), stream)
     dt, ld, code, M, I, off, E, r2r, w = _act_rows(h, act, order, weights, dev)
     if out is None:
-        out, ld_out = torch.empty((M, I), dtype=torch.int8, device=h.device), I
+        out, ld_out = h.new_empty((M, I), dtype=torch.int8), I
     else:
         ld_out = _matrix(out, "out", torch.int8, dev, M, I)
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=h.device)
+        scales = h.new_empty(M, dtype=torch.float32)
         sp = scales.data_ptr()
     else:
         sp = _vector(scales, "scales", dev, (M,))
@@ -931,12 +931,12 @@ def activate_grad(da: torch.Tensor, h: torch.Tensor, act: str = "swiglu", order=
     ld_da = _matrix(da, "da", h.dtype, dev, M, I)
     wide = h.shape[1]
     if out is None:
-        out, ld_out = torch.empty((M, wide), dtype=h.dtype, device=h.device), wide
+        out, ld_out = torch.empty_like(h, memory_format=_ROWS), wide
     else:
         ld_out = _matrix(out, "out", h.dtype, dev, M, wide)
     dw, rt2, dwp = None, None, None
     if w is not None:
-        dw = torch.empty((order.T, order.K), dtype=torch.float32, device=h.device)
+        dw = h.new_empty((order.T, order.K), dtype=torch.float32)
         rt2, dwp = order.route_to_row.data_ptr(), dw.data_ptr()
     _check(_lib.moe_activate_grad(da.data_ptr(), ld_da, h.data_ptr(), ld, dt, code, M, I, off, E, r2r, rt2, w,
                                   out.data_ptr(), ld_out, dwp, _raw_stream(dev)))
@@ -987,13 +987,13 @@ def adapt(base: torch.Tensor, x: torch.Tensor, order: RouteOrder, a: torch.Tenso
     be, ldb = _adapters(b, "b", base.dtype, dev, n, N, r)
     sp = None if scales is None else _vector(scales, "scales", dev, (n,))
     if out is None:
-        out, ld_out = torch.empty((T, N), dtype=base.dtype, device=base.device), N
+        out, ld_out = torch.empty_like(base, memory_format=_ROWS), N
     else:
         ld_out = _matrix(out, "out", base.dtype, dev, T, N)
     size = _lib.moe_adapt_workspace_bytes(T, n, H, r)
     if size == 0:
         raise MoeError(2, _lib.moe_last_error().decode())
-    ws = torch.empty(size, dtype=torch.uint8, device=base.device)
+    ws = base.new_empty(size, dtype=torch.uint8)
     _check(_lib.moe_adapt(base.data_ptr(), ld, x.data_ptr(), ldx, dt, order.row_to_route.data_ptr(),
                           order.route_to_row.data_ptr(), order.offsets.data_ptr(), a.data_ptr(), ae, lda, b.data_ptr(), be,
                           ldb, sp, T, n, H, r, N, ws.data_ptr(), size, out.data_ptr(), ld_out, _raw_stream(dev)))

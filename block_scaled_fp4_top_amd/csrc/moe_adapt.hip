@@ -600,9 +600,12 @@ struct AdaptPlan {
     bool wide;  // the kernels for many tokens an adapter
     int splits;
 };
+// The wide kernels from 2048 tokens and 32 an adapter on. H = 7168, N = 4096, in a graph, us, wide
+// (narrow): rank 16, 1024 tokens of one adapter 17.8 (14.9), 2048 of 64 28.2 (30.2), 4096 of 64
+// 35 (56), of 128 43 (51), of 256 78 (53); rank 64 31 (25), 60 (62), 70 (114), 100 (118), 144 (134).
 static AdaptPlan plan_adapt(int T, int n, int H) {
     AdaptPlan q;
-    q.wide = T >= 64 * (int64_t)std::min(n, T);
+    q.wide = T >= 2048 && T >= 32 * (int64_t)std::min(n, T);
     const int64_t tiles = q.wide ? T / kWideRows + 1 : most_tiles(T, n, 16);
     const int64_t most = std::max((H + kStep * 4 - 1) / (kStep * 4), 1);
     q.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, most, kMaxSplits}));

@@ -322,20 +322,24 @@ __global__ __launch_bounds__(TPT) void rms_norm_grad_kernel(NormGradArgs<T, W> p
     }
 }
 
-// Column sums of the blocks' partial sums, in the order of the blocks within each of four
-// quarters; 64 columns per block.
-__global__ __launch_bounds__(256) void norm_weight_grad_kernel(const float* __restrict__ part, int blocks, int H,
-                                                               float* __restrict__ dweight) {
-    __shared__ float s[4][64];
+// Column sums of the blocks' partial sums, in the order of the blocks within each of sixteen
+// parts; 64 columns per block.
+__global__ __launch_bounds__(1024) void norm_weight_grad_kernel(const float* __restrict__ part, int blocks, int H,
+                                                                float* __restrict__ dweight) {
+    __shared__ float s[16][64];
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
-    const int each = (blocks + 3) / 4, hi = min(blocks, (q + 1) * each);
+    const int each = (blocks + 15) / 16, hi = min(blocks, (q + 1) * each);
     float a = 0.0f;
     if (c < H)
 #pragma unroll 8
         for (int b = q * each; b < hi; ++b) a += part[(size_t)b * H + c];
     s[q][lane] = a;
     __syncthreads();
-    if (q == 0 && c < H) dweight[c] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+    if (q == 0 && c < H) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) a += s[i][lane];
+        dweight[c] = a;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -352,13 +356,21 @@ static hipError_t launch_norm(const NormArgs<T, W>& p, hipStream_t s) {
     hipLaunchKernelGGL((rms_norm_kernel<T, W, TPT, NV>),                                              \
                        dim3(std::min((p.rows + (TPT < 256 ? 256 / TPT : 1) - 1) / (TPT < 256 ? 256 / TPT : 1), 2048)), \
                        dim3(TPT < 256 ? 256 : TPT), 0, s, p)
-    const bool wave = vecs <= 64 || (vecs <= 256 && p.rows >= 4096);
-    if (wave && vecs <= 64) N(64, 1);
-    else if (wave && vecs <= 128) N(64, 2);
-    else if (wave) N(64, 4);
+    // Few rows: many threads each, latency is all there is. Many: as few as hold the row, down to a
+    // wave. Codes, y and residual, bf16, in a graph, us, with 256 threads (512, 1024):
+    // 64 x 7168 9.5 (6.5, 5.8), 256 x 7168 10.1 (7.8, 7.1), 1024 x 7168 17.0 (15.9, 17.9),
+    // 16384 x 7168 208 (210, 223); 64 x 4096 6.2 (4.7, 4.8), 4096 x 4096 27.7 (27.2, 39.6);
+    // 16384 x 2048 64 (75, 140), with a wave 60; 4096 x 2048 17.1 (19.0, 34), with a wave 19.2
+    const bool few = p.rows <= 512, many = p.rows >= 8192;
+    if (vecs <= 64) N(64, 1);
+    else if (many && vecs <= 128) N(64, 2);
+    else if (many && vecs <= 256) N(64, 4);
     else if (vecs <= 256) N(256, 1);
+    else if (few && vecs <= 512) N(512, 1);
     else if (vecs <= 512) N(256, 2);
-    else if (vecs <= 1024) N(256, 4);
+    else if (few && vecs <= 1024) N(1024, 1);
+    else if (vecs <= 1024) N(512, 2);
+    else if (vecs <= 2048) N(1024, 2);
     else if (V == 8 || vecs <= 4096) N(1024, 4);
     else if constexpr (V == 4) N(1024, 8);
 #undef N
@@ -380,7 +392,7 @@ static hipError_t launch_norm_grad(const NormGradArgs<T, W>& p, float* dweight, 
     else if constexpr (V == 4) N(1024, 8);
 #undef N
     if (dweight)
-        hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((p.H + 63) / 64), dim3(256), 0, s, p.part, blocks, p.H, dweight);
+        hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((p.H + 63) / 64), dim3(1024), 0, s, p.part, blocks, p.H, dweight);
     return hipGetLastError();
 }
 

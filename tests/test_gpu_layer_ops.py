@@ -487,9 +487,10 @@ def test_activate_grad_against_differences():
 # ---------------------------------------------------------------------------
 #          T, n, r, H, N
 ADAPTS = [(1, 1, 8, 16, 1), (1, 8, 16, 7168, 4096), (3, 2, 8, 48, 17), (64, 32, 16, 1024, 520), (17, 1024, 8, 64, 100),
-          (70, 3, 40, 208, 300), (33, 4, 256, 320, 257), (200, 2, 64, 512, 130), (500, 3, 72, 144, 70), (300, 1, 16, 2048, 64),
-          (129, 1, 104, 272, 96), (640, 4, 32, 96, 1000), (200, 1, 256, 64, 200), (300, 2, 128, 80, 300), (260, 4, 64, 7168, 137),
-          (130, 1, 8, 400, 128)]
+          (70, 3, 40, 208, 300), (33, 4, 256, 320, 257), (200, 2, 64, 512, 130), (300, 1, 16, 2048, 64), (129, 1, 104, 272, 96),
+          # many tokens an adapter
+          (2100, 3, 64, 208, 300), (2048, 2, 256, 64, 200), (2300, 70, 16, 144, 130), (2200, 1, 104, 272, 96),
+          (2050, 5, 128, 80, 257), (2100, 2, 8, 400, 128), (2049, 4, 40, 2064, 137), (2060, 1, 32, 96, 1000), (2048, 1, 16, 16, 5)]
 
 
 def adapter_case(seed, T, n, r, H, N, dtype, none):
@@ -776,7 +777,7 @@ def test_damaged_maps_stay_in_range():
 
 def test_far_rows():
     """Rows more than 2^31 elements apart."""
-    big = torch.empty((1 << 31) + 4096, dtype=torch.bfloat16, device=DEV)
+    big = torch.empty((1 << 31) + (1 << 22), dtype=torch.bfloat16, device=DEV)
     far = big.as_strided((2, 520), ((1 << 31) + 8, 1))
     far.copy_(torch.randn(2, 520, device=DEV))
     near = far.contiguous()
@@ -789,3 +790,13 @@ def test_far_rows():
     a, b = torch.randn(1, 8, 512, device=DEV).bfloat16(), torch.randn(1, 520, 8, device=DEV).bfloat16()
     one = moe.sort_routes(torch.zeros(2, 1, dtype=torch.int32, device=DEV), 1)
     assert torch.equal(moe.adapt(far, far[:, :512], one, a, b), moe.adapt(near, near[:, :512], one, a, b))
+    # tokens' rows just below and above 4 GiB in all
+    x, base = torch.randn(2048, 64, device=DEV).bfloat16(), torch.randn(2048, 40, device=DEV).bfloat16()
+    a, b = torch.randn(1, 8, 64, device=DEV).bfloat16(), torch.randn(1, 40, 8, device=DEV).bfloat16()
+    one = moe.sort_routes(torch.zeros(2048, 1, dtype=torch.int32, device=DEV), 1)
+    for stride in (1 << 20, (1 << 20) + 1024):
+        far = big.as_strided((2048, 64), (stride, 1))
+        far.copy_(x)
+        # (the two kernels sum in different orders: each within its bound of the other's middle)
+        got, want = moe.adapt(base, far, one, a, b), moe.adapt(base, x, one, a, b)
+        assert torch.equal(got, want) if stride == 1 << 20 else ((got.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -10).all()
