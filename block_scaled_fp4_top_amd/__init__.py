@@ -732,8 +732,8 @@ def route_grad(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, 
     dt = _float_type(logits, "logits")
     ld = _matrix(logits, "logits", logits.dtype, dev)
     T, E = logits.shape
-    if ids.dim() != 2 or ids.shape[0] != T:
-        raise ValueError(f"ids must be [{T}, K], got {tuple(ids.shape)}")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be a tensor [{T}, K]")
     K = ids.shape[1]
     _sizes(T * K)
     dw = _vector(dweights, "dweights", dev, (T, K))

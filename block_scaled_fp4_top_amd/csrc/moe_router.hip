@@ -490,8 +490,13 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs p, int room) {
         // (`best`'s maximum) is the last one's neighbour.
         const float bound = 4.0f + (slack + (BY_LOGITS ? 0.0f : 0x1p-22f * (fabsf(high) + kReach))) * (kKeyUnits / kReach);
         const uint32_t limit = (uint32_t)fminf(bound, 4.0e9f);
-        const uint32_t behind = token_key_max<LPT>(best);
-        bool close = behind && (last >> kIndexBits) - (behind >> kIndexBits) <= limit;
+        // (The same logit and bias make the same key but for the index, which decides then.)
+        auto too_close = [&](uint32_t above, uint32_t below) INLINE {
+            if (!above || !below || (above >> kIndexBits) - (below >> kIndexBits) > limit) return false;
+            const int i = kIndexMask - (above & kIndexMask), j = kIndexMask - (below & kIndexMask);
+            return to_f32(row[i]) != to_f32(row[j]) || (!BY_LOGITS && p.bias && p.bias[i] != p.bias[j]);
+        };
+        bool close = too_close(last, token_key_max<LPT>(best));
 #pragma unroll
         for (int u = 0; u < SLOTS; ++u) {
             if (u * LPT >= p.K) continue;
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs p, int room) {
             uint32_t prior = (uint32_t)__shfl((int)mine[u], (threadIdx.x & 63) - 1);
             const uint32_t wrap = u ? (uint32_t)__shfl((int)mine[u ? u - 1 : 0], (threadIdx.x & 63) | (LPT - 1)) : 0;
             prior = sub ? prior : wrap;
-            if (sub + u * LPT < p.K && mine[u] && prior) close |= (prior >> kIndexBits) - (mine[u] >> kIndexBits) <= limit;
+            if (sub + u * LPT < p.K) close |= too_close(prior, mine[u]);
         }
         if (__ballot(close || !sure)) {
             // Candidates up to one that lies behind a gap, ranked by exact values. Where 64 of them

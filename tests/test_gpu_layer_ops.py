@@ -112,6 +112,25 @@ def test_route_close_choices():
             assert np.array_equal(ids.cpu().numpy(), np.argsort(-x, axis=1))
 
 
+def test_route_equal_logits():
+    """Rows of one value, of the type's lowest, of two values, alone and among others: the lower
+    expert first, also where choices are compared in 64 bits."""
+    for E, K in ((64, 8), (256, 8), (300, 64), (16, 16)):
+        x = rng(E).standard_normal((13, E))
+        x[1], x[2], x[4] = 0.0, -1e9, np.finfo(np.float32).min
+        x[6] = np.where(np.arange(E) % 3 == 0, 1.0, 0.25)
+        x[7, E // 2:] = -1e9
+        for score, bias, G in (("softmax", None, 1), ("sigmoid", np.zeros(E), 1), ("softmax", np.full(E, 0.25), 1),
+                               ("sigmoid", np.tile([0.25, 0.0], E // 2), 4)):
+            for rows in (slice(None), slice(1, 3)):
+                ids, w = moe.route(dev(x[rows], torch.float32), K, score=score, bias=None if bias is None else dev(bias, torch.float32),
+                                   groups=G, top_groups=3 if G > 1 else 1, group_top=2)
+                want_ids, want = ref.route(ref.f32(x[rows]), ids.shape[1], score, bias, G, 3 if G > 1 else 1, 2, True, 1.0)
+                assert np.array_equal(ids.cpu().numpy(), want_ids), (E, score, G)
+                # (distances below 16, up to 64 terms, a dozen operations: below 128 half steps)
+                assert_within(w, want, 128 * U32 * want + 2.0 ** -149, (E, score, G))
+
+
 def test_route_many_tokens():
     """Odd numbers of tokens over many blocks, a broadcast row, no tokens."""
     T, E, K = 5003, 64, 6
