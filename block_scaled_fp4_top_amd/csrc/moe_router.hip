@@ -18,6 +18,13 @@
 // That is the exact order unless two neighbours of it lie closer than the scores' error
 // bound; then the wave goes on to the first gap and ranks these candidates by their exact
 // values.
+//
+// Bound by the vector units: 16383 tokens, 256 experts, K = 8, fp32 (16.8 MB, 3.4 us of
+// memory) 12 us by sigmoid and bias, 13.5 - 18 with 8 groups too (1214 vector instructions
+// for four tokens: 374 the rounds, 186 the groups), 8 us by bf16 logits alone. With fp64 scores
+// and 64-bit rounds throughout 28 us. A launch ends with its slowest wave, so what a few tokens
+// need is kept short: a fallback of a whole wave of tokens to fp64 cost 8 us at the end (and
+// what is left of it is the range above).
 #include <algorithm>
 
 #include "moe_args.h"
@@ -779,6 +786,8 @@ static void with_lanes(int E, bool few, F f) {
     else if (E <= 512) f(L64(), integral_constant<int, 8>());
     else f(L64(), integral_constant<int, 16>());
 }
+// (256 experts, sigmoid and bias, 64 lanes a token against 16, us: 64 tokens 3.7 / 5.2, 1024
+// tokens 5.4 / 7.3, 16383 tokens 15.5 / 12.3)
 constexpr int kFewTokens = 1024;
 
 template <typename X>
