@@ -525,6 +525,7 @@ __global__ __launch_bounds__(256) void adapt_up_wide_kernel(AdaptArgs p, int mos
         have(base);
         if (n0 + kColumns < end) {
             issue(n0 + kColumns, buf ^ 1);
+            asm volatile("" ::: "memory");  // (the count below wants them in this order)
             load_base(n0 + kColumns, next);
         }
         f32x4 acc[MS][8] = {};

@@ -435,6 +435,28 @@ def test_activate_wave_rows():
         assert np.array_equal(codes.cpu().numpy(), codes64) and np.array_equal(f64(scales), s64)
 
 
+def test_activate_blocks_walk_over_rows():
+    """More rows than a launch has blocks, a block's barriers in between: the bits of the same rows
+    alone (codes are exact in any case, gradients sum in an order that the rows do not change)."""
+    g = rng(12)
+    for dtype, R, I in ((torch.bfloat16, 8700, 2064), (torch.float32, 8500, 1029)):
+        h, da = dev(g.standard_normal((R, 2 * I)), dtype), dev(g.standard_normal((R, I)), dtype)
+        h[5, :I] = -40.0  # (by the exact way)
+        weights = dev(g.standard_normal((R, 1)).astype(np.float32))
+        one = lambda n: moe.sort_routes(torch.zeros(n, 1, dtype=torch.int32, device=DEV), 1)
+        order = one(R)
+        codes, scales = moe.activate_int8(h, order=order, weights=weights)
+        out = moe.activate(h, order=order, weights=weights)
+        dh, dw = moe.activate_grad(da, h, order=order, weights=weights)
+        for lo in (0, 4000, R - 600):
+            s, part = slice(lo, lo + 600), one(600)
+            c, sc = moe.activate_int8(h[s], order=part, weights=weights[s])
+            assert torch.equal(c, codes[s]) and torch.equal(sc, scales[s])
+            assert torch.equal(moe.activate(h[s], order=part, weights=weights[s]), out[s])
+            d, w = moe.activate_grad(da[s], h[s], order=part, weights=weights[s])
+            assert torch.equal(d, dh[s]) and torch.equal(w, dw[s])
+
+
 def test_activate_codes_next_to_a_half():
     """relu2 of integers: many exact halves (ties to even), and values that fp32 rounds onto
     the wrong side: rows whose largest square is 127 * 2^k."""
@@ -543,6 +565,30 @@ def test_adapt(T, n, r, H, N, dtype):
         assert torch.equal(fresh, got)
         here = base.clone() if pad == 0 else base
         moe.adapt(here, x, order, a_t, b_t, dev(scales), out=here)  # in place
+        assert torch.equal(here, got)
+
+
+#                 T, n, r, H, N: blocks that walk over several pieces of the columns
+WALKS = [(4100, 3, 24, 64, 4100), (9000, 5, 72, 64, 2600), (6000, 4, 256, 48, 3333), (16000, 2, 16, 16, 2000),
+         (1500, 200, 72, 64, 2000), (1900, 300, 16, 64, 4000)]
+
+
+@pytest.mark.parametrize("T,n,r,H,N", WALKS)
+@pytest.mark.parametrize("dtype", DT[:2], ids=NAME.get)
+def test_adapt_many_columns(T, n, r, H, N, dtype):
+    say("adapt", T, n, r, H, N, NAME[dtype])
+    part = 2.0 ** -16 if dtype == torch.bfloat16 else 2.0 ** -21
+    ids, base, x, a, b, scales = adapter_case(T + r, T, n, r, H, N, dtype, 0.1)
+    base, x, a, b = dev(base, dtype), dev(x, dtype), dev(a, dtype), dev(b, dtype)
+    order = moe.sort_routes(dev(ids.astype(np.int32)[:, None]), n)
+    got = moe.adapt(base, x, order, a, b, dev(scales))
+    some = np.unique(np.concatenate([np.arange(200), rng(1).integers(0, T, 300), [T - 1]]))
+    want, bound = ref.adapt(f64(base)[some], f64(x)[some], ids[some], f64(a), f64(b), scales.astype(np.float64), part)
+    assert_within(got[torch.from_numpy(some).to(DEV)], want,
+                  np.where((ids[some] >= 0)[:, None], stored(bound, want, dtype), 0.0), "adapt")
+    for _ in range(3):
+        here = base.clone()
+        moe.adapt(here, x, order, a, b, dev(scales), out=here)
         assert torch.equal(here, got)
 
 
