@@ -84,7 +84,7 @@ __device__ __forceinline__ void row_reduce(float* ss, uint32_t* top, float (*s_s
 // A row per TPT threads (a wave, or a block); each thread keeps its NV vectors of 16
 // bytes between the sum and the output, so a row is read once. Blocks walk over rows.
 // Bound by memory: 16384 x 7168 bf16 with residual, y and codes (1.06 GB) 206 us, 5.1 TB/s;
-// y alone 92 us. 64 x 7168: 5.1 us, latency.
+// y alone 91 us. 64 x 7168: 5.6 us, latency.
 template <typename T, typename W, int TPT, int NV>
 __global__ __launch_bounds__(TPT < 256 ? 256 : TPT) void rms_norm_kernel(NormArgs<T, W> p) {
     constexpr int V = 16 / sizeof(T), PER = TPT < 256 ? 256 / TPT : 1;
@@ -194,8 +194,8 @@ __global__ __launch_bounds__(TPT < 256 ? 256 : TPT) void rms_norm_kernel(NormArg
 // With n = h r and g = dy w:  dx = r (g - n mean(g n)) (+ dtotal),  dw = sum over rows of dy n.
 // dw: every block sums its rows in registers, in order, and leaves one row of partial
 // sums in the workspace, which a second kernel adds in the order of the blocks.
-// Bound by memory: 4096 x 4096 bf16 with dtotal (134 MB and 17 MB of partial sums) 24.4 and
-// 4.2 us, 16384 x 7168 without (705 MB) 140 us. In a graph 25 and 141 us with 512 blocks, 29 and 161 with
+// Bound by memory: 4096 x 4096 bf16 with dtotal (134 MB and 17 MB of partial sums) 26.8 and
+// 4.3 us from memory, 16384 x 7168 without (705 MB) 140 us. In a graph 25 and 141 us with 512 blocks, 29 and 161 with
 // 256 (too little on its way), 25 and 156 with 1024 (partial sums).
 template <typename T, typename W>
 struct NormGradArgs {
