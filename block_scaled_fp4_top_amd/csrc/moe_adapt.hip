@@ -5,10 +5,12 @@
 // Two launches. The first multiplies the tokens of one adapter with its a[e] ([r][H]); the
 // depth is split over blocks where there are few tokens, each leaving one fp32 partial
 // sum of v = a x in the workspace. The second adds them in a fixed order and multiplies
-// with b[e] ([N][r]). v stays as exact as fp32 there: it is split in two parts of the
-// operands' type, hi + lo (16 bits or more of it), which costs a second matrix
-// instruction where the matrix cores have nothing else to do. fp16 parts are scaled by a
-// power of two per token, as v may lie outside fp16's range.
+// with b[e] ([N][r]). v stays what it is in fp32: three parts of the operands' type, each the
+// rounded rest of those before it, hold all 24 bits (3 x 8 in bf16, 11 + 11 + 2 in fp16), at
+// the price of two more matrix instructions where the matrix cores have nothing else to do.
+// (With two parts, 17 bits in bf16, seven of 4096 columns of a token were rounded to the other
+// neighbour.) fp16 parts are scaled by a power of two per token, as v may lie outside fp16's
+// range; they end 2^-37 below the token's largest |v|.
 //
 // A lane's part of a matrix operand is 8 consecutive elements of row lane % 16, so 16
 // neighbouring lanes read 16 rows: straight from memory that costs the address units about
@@ -182,12 +184,14 @@ __device__ __forceinline__ void copy_tokens(const AdaptArgs& p, int group) {
 // infinity, NaN: as they are)
 __device__ __forceinline__ int power_for(uint32_t top) { return top && top < 0x7F800000u ? 12 - ilogbf(u2f(top)) : 0; }
 
-// f as hi + lo of type T (an infinity or a NaN in hi alone)
+// f as hi + mid + lo of type T (an infinity or a NaN in hi alone). The rests are exact: what a
+// rounding leaves of a float is a float.
 template <typename T>
-__device__ __forceinline__ void split_value(float f, T* hi, T* lo) {
+__device__ __forceinline__ void split_value(float f, T* hi, T* mid, T* lo) {
     *hi = from_f32<T>(f);
-    const float h = to_f32(*hi);
-    *lo = from_f32<T>(fabsf(h) < __builtin_huge_valf() ? f - h : 0.0f);
+    const float h = to_f32(*hi), rest = fabsf(h) < __builtin_huge_valf() ? f - h : 0.0f;
+    *mid = from_f32<T>(rest);
+    *lo = from_f32<T>(rest - to_f32(*mid));
 }
 
 template <typename T, int MS, int KS>
@@ -234,10 +238,10 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
         for (int s = 0; s < KR; ++s) load_b(first, 32 * s + 8 * q, bv[s]);
     }
     load_base(first);
-    // v: fp32 [BM][wide], then its parts hi and lo [BM][wide] each
+    // v: fp32 [BM][wide], then its parts hi, mid and lo [BM][wide] each
     const int deep = KS ? 32 * KS : (p.r + 31) / 32 * 32, wide = deep + 8;
     float* v = (float*)s_room;
-    T *v_hi = (T*)(v + BM * wide), *v_lo = v_hi + BM * wide;
+    T *v_hi = (T*)(v + BM * wide), *v_mid = v_hi + BM * wide, *v_lo = v_mid + BM * wide;
     {
         constexpr int TPR = 256 / BM;  // threads of a row
         const int row = tid / TPR, at = tid % TPR;
@@ -268,8 +272,10 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
         if (at == 0) s_back[row] = ldexpf(p.scales ? p.scales[e] : 1.0f, -up);
         for (int j = at * 4; j < deep; j += TPR * 4)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                split_value(ldexpf(v[row * wide + j + i], up), &v_hi[row * wide + j + i], &v_lo[row * wide + j + i]);
+            for (int i = 0; i < 4; ++i) {
+                const int at = row * wide + j + i;
+                split_value(ldexpf(v[at], up), &v_hi[at], &v_mid[at], &v_lo[at]);
+            }
     }
     __syncthreads();
     for (int i = 0; i < chunks; ++i) {
@@ -281,9 +287,10 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
 #pragma unroll
             for (int m = 0; m < MS; ++m) {
                 const Vec<T> hi = *reinterpret_cast<const Vec<T>*>(v_hi + (m * 16 + c) * wide + k);
+                const Vec<T> mid = *reinterpret_cast<const Vec<T>*>(v_mid + (m * 16 + c) * wide + k);
                 const Vec<T> lo = *reinterpret_cast<const Vec<T>*>(v_lo + (m * 16 + c) * wide + k);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) acc[m][u] = mma(w[u], hi, mma(w[u], lo, acc[m][u]));
+                for (int u = 0; u < 4; ++u) acc[m][u] = mma(w[u], hi, mma(w[u], mid, mma(w[u], lo, acc[m][u])));
             }
         };
         if constexpr (KS > 0) {
@@ -425,8 +432,12 @@ __global__ __launch_bounds__(256) void adapt_down_wide_kernel(AdaptArgs p, uint3
 // whose v waits in registers. Lane (c, q) holds columns 8 c .. 8 c + 7 of tokens 4 q .. 4 q + 3:
 // row 8 c + u of b is column c of instruction u and lies in row 16 u + c of the buffer, its
 // chunks mixed (where their number is a power of two) so that 16 rows use all banks.
+//
+// Ranks of 65 to 128 take 264 registers, of which 256 let two waves of a SIMD run: held to
+// them (six are spilled) the call of 16384 tokens, H = 7168, N = 4096, rank 128, takes 228 us
+// instead of 268.
 template <typename T, int MS, int KS>
-__global__ __launch_bounds__(256) void adapt_up_wide_kernel(AdaptArgs p, int most, int nblocks, int chunks) {
+__global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(AdaptArgs p, int most, int nblocks, int chunks) {
     constexpr int BM = 64 * MS, kColumns = 128;
     extern __shared__ __align__(1024) char s_room[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
@@ -454,7 +465,7 @@ __global__ __launch_bounds__(256) void adapt_up_wide_kernel(AdaptArgs p, int mos
     const uint32_t room = lds_address(s_room);
     issue(first, 0);
     // v of the wave's rows (those behind the last are the last one's again)
-    Vec<T> hi[MS][KS], lo[MS][KS];
+    Vec<T> hi[MS][KS], mid[MS][KS], lo[MS][KS];
     float back[MS][4];
     int token[MS][4];
 #pragma unroll
@@ -494,7 +505,7 @@ __global__ __launch_bounds__(256) void adapt_up_wide_kernel(AdaptArgs p, int mos
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) split_value(ldexpf(f[s][i], up), &hi[m][s].e[i], &lo[m][s].e[i]);
+            for (int i = 0; i < 8; ++i) split_value(ldexpf(f[s][i], up), &hi[m][s].e[i], &mid[m][s].e[i], &lo[m][s].e[i]);
     }
     // Base of a pass, always MS * 4 loads (none where a row has no 8 columns: then there is one
     // pass), so that the wait below can count them.
@@ -543,7 +554,7 @@ __global__ __launch_bounds__(256) void adapt_up_wide_kernel(AdaptArgs p, int mos
                 if (p.r % 32 && k >= rc) v[u] = u32x4{};
                 const Vec<T> bv = __builtin_bit_cast(Vec<T>, v[u]);
 #pragma unroll
-                for (int m = 0; m < MS; ++m) acc[m][u] = mma(hi[m][s], bv, mma(lo[m][s], bv, acc[m][u]));
+                for (int m = 0; m < MS; ++m) acc[m][u] = mma(hi[m][s], bv, mma(mid[m][s], bv, mma(lo[m][s], bv, acc[m][u])));
             }
         }
         const int n = n0 + 8 * c;
@@ -651,7 +662,7 @@ static hipError_t launch_up(const AdaptArgs& p, bool wide, hipStream_t s) {
     const int chunks = (int)std::min<int64_t>(std::max<int64_t>(most * columns / 1024, 1), wide ? 16 : 8);
     const int nblocks = (int)((columns + chunks - 1) / chunks);
     const int copy = p.out == p.base ? 0 : (p.T + kCopyTokens - 1) / kCopyTokens;
-    const int lds = wide ? 2 * 128 * p.r * 2 : 16 * ((p.r + 31) / 32 * 32 + 8) * 8;
+    const int lds = wide ? 2 * 128 * p.r * 2 : 16 * ((p.r + 31) / 32 * 32 + 8) * 10;
 #define U(KERNEL)                                                                                                      \
     hipLaunchKernelGGL((KERNEL), dim3((int)most * nblocks + copy), dim3(256), lds, s, p, (int)most, nblocks, chunks)
     if (wide) {

@@ -428,8 +428,9 @@ size_t moe_adapt_workspace_bytes(int32_t T, int32_t adapters, int32_t H, int32_t
 
 /* Low-rank adapters of many requests beside a shared projection:
  *   out[t] = base[t] + scales[e] b[e] (a[e] x[t]), e the adapter of token t, and
- *   out[t] = base[t] (bit for bit) for a token without one. Sums and a[e] x[t] in fp32,
- *   one rounding. (An infinity in b makes its column infinite or NaN.)
+ *   out[t] = base[t] (bit for bit) for a token without one. Sums and a[e] x[t] in fp32
+ *   (with fp16 operands to 2^-37 of the token's largest |a[e] x[t]|), one rounding. (An
+ *   infinity in b makes its column infinite or NaN.)
  *   base, out: [T][N], x: [T][H], a: [adapters][rank][H], b: [adapters][N][rank], all of
  *   type dtype (bf16 or fp16); rows of a and b a_stride and b_stride apart, adapters
  *   a_adapter_stride and b_adapter_stride (0: one for all, to 2^48). scales: [adapters]
