@@ -372,7 +372,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs p, int room) {
     const X* row = (const X*)p.logits + (int64_t)(live ? t : p.T - 1) * p.ld;  // (lanes without a token do another's work)
     float x[EPL], bias[EPL];
     load_logits<EPL>(row, first, p.E, x);
-    if (!BY_LOGITS) {
+    auto load_bias = [&]() INLINE {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) bias[i] = 0.0f;
         if (p.bias) {
@@ -385,7 +385,8 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs p, int room) {
                     if (first + i < p.E) bias[i] = p.bias[first + i];
             }
         }
-    }
+    };
+    if (!BY_LOGITS) load_bias();
     bool nan = false;
     float top = -kInf, sum = 0.0f;  // of the softmax
     float c[EPL], slack = 0.0f;     // choices, and twice what they may be off
@@ -497,13 +498,32 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs p, int room) {
         // (`best`'s maximum) is the last one's neighbour.
         const float bound = 4.0f + (slack + (BY_LOGITS ? 0.0f : 0x1p-22f * (fabsf(high) + kReach))) * (kKeyUnits / kReach);
         const uint32_t limit = (uint32_t)fminf(bound, 4.0e9f);
-        // (The same logit and bias make the same key but for the index, which decides then.)
+        auto near = [&](uint32_t above, uint32_t below) INLINE {
+            return above && below && (above >> kIndexBits) - (below >> kIndexBits) <= limit;
+        };
+        // The same logit and bias make the same key but for the index, which decides then: these two
+        // stand as they are, but say nothing of what follows them. Among the keys taken the next
+        // pair does; across the last place, the first key behind it of another choice.
         auto too_close = [&](uint32_t above, uint32_t below) INLINE {
-            if (!above || !below || (above >> kIndexBits) - (below >> kIndexBits) > limit) return false;
+            if (!near(above, below)) return false;
             const int i = kIndexMask - (above & kIndexMask), j = kIndexMask - (below & kIndexMask);
             return to_f32(row[i]) != to_f32(row[j]) || (!BY_LOGITS && p.bias && p.bias[i] != p.bias[j]);
         };
-        bool close = too_close(last, token_key_max<LPT>(best));
+        const uint32_t rest = token_key_max<LPT>(best);
+        bool close = too_close(last, rest);
+        const bool run = !close && near(last, rest);
+        if (__ballot(run)) {
+            asm volatile("" ::: "memory");  // (loads again, instead of registers for the biases until here)
+            load_logits<EPL>(row, first, p.E, x);
+            if (!BY_LOGITS) load_bias();
+            const int at = run ? kIndexMask - (last & kIndexMask) : 0;
+            const float l = to_f32(row[at]), b = !BY_LOGITS && p.bias ? p.bias[at] : 0.0f;
+            uint32_t other = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (key[i] < last && (x[i] != l || (!BY_LOGITS && bias[i] != b))) other = max(other, key[i]);
+            close |= run && near(last, token_key_max<LPT>(other));
+        }
 #pragma unroll
         for (int u = 0; u < SLOTS; ++u) {
             if (u * LPT >= p.K) continue;

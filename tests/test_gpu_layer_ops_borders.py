@@ -62,3 +62,59 @@ def test_adapt_keeps_every_bit_between_the_products(T, r, dtype):
         got = moe.adapt(torch.zeros(T, N, dtype=dtype, device=DEV), dev(x * size[:, None], dtype), order, dev(a, dtype),
                         dev(b, dtype), torch.full((1,), 1024.0, device=DEV))
         assert np.array_equal(f64(got), np.repeat((1024.0 * last * size)[:, None], N, axis=1)), at
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+BORDERS = [([0.0, -50.0, -50.0, -40.0], 2), ([0.0, -1e4, -1e4, -40.0], 2), ([1.0, 1.0, 1.0 + 2.0 ** -21, -3.0], 1),
+           ([16.0, 16.0, 16.125, -3.0], 1), ([20.0, 0.0, 0.0, 3.0], 2), ([5.0] * 9 + [5.0 + 2.0 ** -20] + [5.0] * 3, 4)]
+
+
+@pytest.mark.parametrize("E", [16, 64, 128, 256, 300, 1024])
+@pytest.mark.parametrize("T", [6, 1100])  # (lanes of a token: 64, and 16 up to 256 experts)
+def test_route_equal_choices_across_the_last_place(E, T):
+    """Equal experts on both sides of the last place, and a better one behind them that the fast
+    comparison cannot tell from them."""
+    say("route borders", E, T)
+    g = rng(E + T)
+    for dtype in DT:
+        for row, K in BORDERS:
+            x = np.full((min(T, 60), E), -np.inf)
+            for t in range(len(x)):  # spread over the experts, in this order; the rest masked or far below
+                at = np.arange(len(row)) if t < 2 else np.sort(g.permutation(E)[:len(row)])
+                x[t] = -np.inf if t % 2 else -1e5 if dtype != torch.float16 else -6e4
+                x[t, at] = row
+            xt = over(dev(x, dtype), T)
+            for score in ("softmax", "sigmoid"):
+                for bias in (None, np.zeros(E), np.full(E, 0.25)):
+                    ids, w = moe.route(xt, K, score=score, bias=None if bias is None else dev(bias, torch.float32))
+                    want_ids, want = ref.route(f64(xt[:len(x)]), K, score, bias, 1, 1, 1, True, 1.0)
+                    want_ids, want = over(want_ids, T), over(want, T)
+                    assert np.array_equal(ids.cpu().numpy(), want_ids), (dtype, row, score, bias is None)
+                    # (what is not 0 lies less than 104 below the top: 104 half steps of the difference, 50
+                    # of the exponent, the sum and a dozen operations)
+                    assert_within(w, want, 200 * U32 * want + 2.0 ** -126, (dtype, row, score))
+
+
+@pytest.mark.parametrize("E,G", [(16, 4), (64, 8), (128, 8), (256, 16), (160, 5), (300, 50), (1024, 16)])
+def test_route_few_values(E, G):
+    """Rows of a few values only, some next to each other, with and without equal biases and
+    groups: every border lies in a run of equal experts."""
+    say("route few values", E, G)
+    g = rng(E)
+    for T in (37, 1100):
+        sets = [[0.0, -50.0, -40.0, -1e4], [1.0, 1.0 + 2.0 ** -21, 0.5], [16.0, 16.125, -3.0], [20.0, 0.0, 3.0, -np.inf]]
+        x = np.stack([g.choice(sets[t % 4], E) for t in range(min(T, 60))])
+        xt = over(dev(x, torch.float32), T)
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, np.zeros(E), np.full(E, 0.25), g.choice([0.0, 0.25], E)):
+                for groups, best in ((1, 1), (G, 1), (G, 2)):
+                    if best == 2 and bias is not None and len(set(bias)) > 1:
+                        continue  # (sums of the same scores and biases in another order: equal but for roundings)
+                    K = int(g.integers(1, 9))
+                    top = min(3, groups)
+                    ids, _ = moe.route(xt, K, score=score, bias=None if bias is None else dev(bias, torch.float32), groups=groups,
+                                       top_groups=top, group_top=best)
+                    want_ids, _ = ref.route(f64(xt[:len(x)]), K, score, bias, groups, top, best, True, 1.0)
+                    assert np.array_equal(ids.cpu().numpy(), over(want_ids, T)), (T, score, bias is None, groups, best, K)
