@@ -455,10 +455,12 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
     auto mix = [&](int row) INLINE { return shift < 0 ? 0 : shift >= 3 ? (row >> 1) & 7 : (row >> (4 - shift)) & ((1 << shift) - 1); };
     const T* b = (const T*)p.b + e * p.b_adapter;
     auto issue = [&](int n0, int buf) INLINE {
+        const int last = min(kColumns, p.N - n0) - 1;  // (rows may share memory: their stride may lie below the rank)
+        const uint32_t bytes = (uint32_t)(last * p.ld_b + p.r) * 2;
         for (int i = wave; i < 2 * rc; i += 4) {
             const int slot = i * 64 + lane, at = slot / rc, chunk = (slot - at * rc) ^ mix(at & 15);
-            const int n = min(8 * (at & 15) + (at >> 4), p.N - 1 - n0);
-            buffer_load_lds16<false>(b + n0 * p.ld_b, 128u * (uint32_t)(p.ld_b * 2), (uint32_t)n * (uint32_t)(p.ld_b * 2) + chunk * 16,
+            const int n = min(8 * (at & 15) + (at >> 4), last);
+            buffer_load_lds16<false>(b + n0 * p.ld_b, bytes, (uint32_t)n * (uint32_t)(p.ld_b * 2) + chunk * 16,
                                      s_room + buf * size + i * 1024);
         }
     };

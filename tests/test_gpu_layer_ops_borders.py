@@ -64,6 +64,43 @@ def test_adapt_keeps_every_bit_between_the_products(T, r, dtype):
         assert np.array_equal(f64(got), np.repeat((1024.0 * last * size)[:, None], N, axis=1)), at
 
 
+@pytest.mark.parametrize("T,r,N", [(40, 16, 300), (2048, 16, 300), (2100, 64, 130), (2050, 104, 257), (2048, 256, 128)])
+@pytest.mark.parametrize("dtype", DT[:2], ids=NAME.get)
+def test_adapt_rows_of_b_that_share_memory(T, r, N, dtype):
+    """Row strides of b (and of a) below the rank: one row for all columns, rows that overlap,
+    on both sides of where the wide kernels begin."""
+    say("adapt strides", T, r, N, NAME[dtype])
+    n, H = 2, 64
+    g = rng(T + r)
+    ids = g.integers(0, n, T)
+    base, x = dev(g.standard_normal((T, N)), dtype), dev(g.standard_normal((T, H)), dtype)
+    pool = dev(g.standard_normal(2 * (N + 1) * r + r * H) / r ** 0.5, dtype)
+    a = dev(g.standard_normal((n, r, H)) / H ** 0.5, dtype)
+    order = moe.sort_routes(dev(ids.astype(np.int32)[:, None]), n)
+    for ld in (0, 1, 4, 8, r - 1):
+        b = pool.as_strided((n, N, r), (N * ld + r, ld, 1))
+        for a_t in (a, a[:, :1].expand(n, r, H), pool.as_strided((n, r, H), (r * 8, 8, 1))):
+            got = moe.adapt(base, x, order, a_t, b)
+            assert torch.equal(got, moe.adapt(base, x, order, a_t.contiguous(), b.contiguous())), ld
+            want, bound = ref.adapt(f64(base), f64(x), ids, f64(a_t), f64(b), np.ones(n), 0.0 if dtype == torch.bfloat16 else 2.0 ** -23)
+            assert_within(got, want, stored(bound, want, dtype), ld)
+
+
+@pytest.mark.parametrize("T", [64, 2048])
+@pytest.mark.parametrize("dtype", DT[:2], ids=NAME.get)
+def test_adapt_one_column(T, dtype):
+    """N = 1: b as a transposed view, whose row stride is 1 (no row follows)."""
+    n, r, H = 3, 256, 64
+    g = rng(T)
+    base, x, a = dev(g.standard_normal((T, 1)), dtype), dev(g.standard_normal((T, H)), dtype), dev(g.standard_normal((n, r, H)), dtype)
+    w = dev(g.standard_normal((n, r)) / 64, dtype)
+    order = moe.sort_routes(dev(g.integers(0, n, (T, 1)).astype(np.int32)), n)
+    b = w.view(n, r, 1).transpose(1, 2)
+    assert b.stride(1) == 1
+    got = moe.adapt(base, x, order, a, b)
+    assert torch.equal(got, moe.adapt(base, x, order, a, w.clone().view(n, 1, r))) and not torch.equal(got, base)
+
+
 # ---------------------------------------------------------------------------
 # routing
 # ---------------------------------------------------------------------------
