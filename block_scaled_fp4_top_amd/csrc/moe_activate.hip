@@ -120,14 +120,17 @@ __global__ __launch_bounds__(RowThreads<TPT>::kBlock) void act_kernel(ActArgs p)
 //
 // kActError, relative, from kDeep on: exp2's argument is off by 1.25 |g| half steps (2^-24), exp2
 // and the reciprocal by 2 each, 1 + e, both products and the quotient by 5.5 in all: 30
-// half steps at g = -16. Gates below kDeep go the exact way.
+// half steps at g = -16. Gates below kDeep go the exact way. The sigmoid meets u first: it lies
+// between 1e-7 and 1 here, while g sigmoid(g) of a subnormal g would keep few bits. (What
+// sigmoid(g) u loses below 2^-126 shows in the product only where g is beyond 2^36, whose
+// sigmoid is 1 and loses nothing.)
 constexpr float kActError = 0x1p-19f;
 constexpr float kDeep = -16.0f;
 constexpr float kSmallAct = 0x1p-90f;
 
 template <bool SWIGLU>
 __device__ __forceinline__ float act_fast(float g, float u) {
-    if constexpr (SWIGLU) return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+    if constexpr (SWIGLU) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u * g;
     const float z = fmaxf(g, 0.0f);
     return g != g ? g : z * z;
 }
@@ -143,7 +146,9 @@ __device__ __forceinline__ double act_exact(double g, double u) {
 
 // Four waves per SIMD (128 registers) for rows of a wave each: 65536 x 2048 bf16 161 -> 142 us,
 // 16384 x 2048 from memory 49 -> 44 (3.8 TB/s; 141 registers let three run, five spill: 117).
-// Bound by memory and by the vector units, which are half busy.
+// Bound by memory and by the vector units. Gates below kDeep cost more, as a vector that
+// has one is computed again: with gates of deviation 6 (0.4 % of them) 16384 x 2048 35 -> 73 us,
+// and the wave of a row that lies there altogether takes 70 us longer than others.
 template <typename T, bool SWIGLU, int TPT, int NV>
 __global__ __launch_bounds__(RowThreads<TPT>::kBlock, TPT == 64 ? 4 : 1) void act_int8_kernel(ActArgs p) {
     constexpr int V = 16 / sizeof(T), NW = RowThreads<TPT>::kWaves;

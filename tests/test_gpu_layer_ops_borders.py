@@ -155,3 +155,28 @@ def test_route_few_values(E, G):
                                        top_groups=top, group_top=best)
                     want_ids, _ = ref.route(f64(xt[:len(x)]), K, score, bias, groups, top, best, True, 1.0)
                     assert np.array_equal(ids.cpu().numpy(), over(want_ids, T)), (T, score, bias is None, groups, best, K)
+
+
+# ---------------------------------------------------------------------------
+# activation
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("I", [7, 300, 2048, 5000])
+def test_activate_codes_of_subnormal_gates(I):
+    """Gates below fp32's normal range (silu there is half of a few steps) times large ups: the
+    codes are those of the product in 64 bits."""
+    say("subnormal gates", I)
+    g = rng(I)
+    for dtype in (torch.float32, torch.bfloat16):
+        step = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133
+        for rows in (6, 4100 if I == 300 else 6):
+            h = np.concatenate([g.integers(-9, 10, (rows, I)) * step, g.standard_normal((rows, I)) * 2.0 ** 100], axis=1)
+            h[1, I:] *= 2.0 ** 27 / np.abs(h[1, I:]).max() * 2.0 ** 100
+            h[2, I // 2] = 2.0 ** -100  # among others
+            h[3, :I] = step             # 0 after one rounding of silu
+            h[4, :I] = g.standard_normal(I) * 2.0 ** -128
+            h[5, I:] = 1.0              # too small for a scale
+            ht = dev(h, dtype)
+            codes, scales = moe.activate_int8(ht)
+            codes64, s64 = ref.quantize(ref.activation(f64(ht), "swiglu"))
+            assert np.array_equal(f64(scales), s64), dtype
+            assert np.array_equal(codes.cpu().numpy(), codes64), dtype
