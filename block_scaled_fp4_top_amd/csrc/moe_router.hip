@@ -253,6 +253,11 @@ __device__ __forceinline__ bool groups_of_lanes(int epl, int S) {
 // The same by fp32 choices c (-inf: none). False if a group that stays lies within the error
 // bound of one that goes: `slack` for the scores of both, and four roundings of each
 // group's two choices (slack 0: c is exact, ties go to the lower group).
+// A sum of two of the lowest values counts as the lowest, not as -inf: such a group has something
+// to choose (and its error bound sends it to the exact choice).
+__device__ __forceinline__ float group_score(const Top2<float>& t, int group_top) {
+    return group_top == 2 && t.b > -kInf ? fmaxf(t.a + t.b, kLowest) : t.a;
+}
 __device__ __forceinline__ float lowest_of(float score, const Top2<float>& t, float slack) {
     return score - (slack + 0x1p-22f * (fabsf(t.a) + (t.b > -kInf ? fabsf(t.b) : 0.0f)));
 }
@@ -280,7 +285,7 @@ __device__ __forceinline__ bool keep_groups_fast(const RouteArgs& p, int sub, fl
         if (n > 2) join(dpp_move<0x4E>(t.a), dpp_move<0x4E>(t.b));    // lane ^ 2
         if (n > 4) join(dpp_move<0x141>(t.a), dpp_move<0x141>(t.b));  // mirrored in 8 lanes
         if (n > 8) join(dpp_move<0x140>(t.a), dpp_move<0x140>(t.b));  // in 16
-        score = p.group_top == 2 && t.b > -kInf ? t.a + t.b : t.a;
+        score = group_score(t, p.group_top);
         if (first_expert<EPL>(sub) >= p.E) score = -kInf;
         int better = 0;
         // (lanes of the same group have the same score and are no better)
@@ -322,7 +327,7 @@ __device__ __forceinline__ bool keep_groups_fast(const RouteArgs& p, int sub, fl
             t.b = __builtin_amdgcn_fmed3f(t.a, t.b, v);
             t.a = fmaxf(t.a, v);
         }
-        scores[h] = p.group_top == 2 && t.b > -kInf ? t.a + t.b : t.a;
+        scores[h] = group_score(t, p.group_top);
         // (the group's own choices are no longer needed: its error bound instead)
         choice[h * pad] = lowest_of(scores[h], t, slack);
         if (S > 1) choice[h * pad + 1] = highest_of(scores[h], t, slack);

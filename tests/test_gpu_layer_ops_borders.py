@@ -157,6 +157,26 @@ def test_route_few_values(E, G):
                     assert np.array_equal(ids.cpu().numpy(), over(want_ids, T)), (T, score, bias is None, groups, best, K)
 
 
+@pytest.mark.parametrize("E,G", [(8, 4), (64, 8), (128, 8), (256, 16), (160, 5), (300, 50), (1024, 16)])
+@pytest.mark.parametrize("T", [5, 1100])
+def test_route_groups_of_lowest_choices(E, G, T):
+    """Groups whose best two choices count as the lowest value, or are biases near it: their sum
+    lies below fp32's range, and yet above a group with nothing to choose."""
+    say("route lowest groups", E, G, T)
+    S = E // G
+    bias = np.zeros(E)
+    bias[-S:] = -3e38
+    x = np.full((T, E), -np.inf)
+    x[0::2, S:2 * S] = np.nan      # groups 0 and 2 on: nothing to choose
+    x[1::2, -S:] = 1.0             # the last group alone, by its bias
+    for score in ("softmax", "sigmoid"):
+        ids, w = moe.route(dev(x, torch.float32), 2, score=score, bias=dev(bias, torch.float32), groups=G, top_groups=1, group_top=2)
+        want = np.where((np.arange(T) % 2 == 0)[:, None], [[S, S + 1]], [[E - S, E - S + 1]])
+        assert np.array_equal(ids.cpu().numpy(), want), score
+        w = f64(w)
+        assert np.isnan(w[0::2]).all() and np.array_equal(w[1::2], np.full(w[1::2].shape, 0.5))
+
+
 # ---------------------------------------------------------------------------
 # activation
 # ---------------------------------------------------------------------------
