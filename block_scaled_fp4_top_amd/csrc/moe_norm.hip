@@ -158,7 +158,8 @@ __global__ __launch_bounds__(TPT < 256 ? 256 : TPT) void rms_norm_kernel(NormArg
             set ^= 1;
             row_reduce<TPT>(&ss, &top, s_sum, s_top, set);
         }
-        const float r = inverse_rms(ss, f, p.H, p.eps);
+        float r = inverse_rms(ss, f, p.H, p.eps);
+        if (f < 1.0f) r *= f, f = 1.0f;  // (a row of large values: h f would take the bits of its small ones)
         if (p.y) {
             T* y = p.y + m * p.ld_y;
 #pragma unroll
@@ -290,8 +291,9 @@ __global__ __launch_bounds__(TPT) void rms_norm_grad_kernel(NormGradArgs<T, W> p
             set ^= 1;
             sums();
         }
-        const float r = inverse_rms(ss, f, p.H, p.eps);
+        float r = inverse_rms(ss, f, p.H, p.eps);
         const float mean = __fdiv_rn(sg * r, (float)p.H);  // of g n
+        if (f < 1.0f) r *= f, f = 1.0f;  // (as in rms_norm_kernel)
         T* dx = p.dx + m * p.ld_dx;
         auto one = [&](float d, float v, float wt, float more, float* sum) INLINE {
             const float n = v * f * r;

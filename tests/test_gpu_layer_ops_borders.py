@@ -200,3 +200,34 @@ def test_activate_codes_of_subnormal_gates(I):
             codes64, s64 = ref.quantize(ref.activation(f64(ht), "swiglu"))
             assert np.array_equal(f64(scales), s64), dtype
             assert np.array_equal(codes.cpu().numpy(), codes64), dtype
+
+
+# ---------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("H", [33, 2000, 5000])
+def test_norm_small_values_beside_large_ones(H):
+    """Rows whose squares leave fp32's range keep the bits of their small values."""
+    say("norm small beside large", H)
+    g = rng(H)
+    h = g.standard_normal((6, H)) * 2.0 ** np.array([-45, -48, -40, -30, 0, -50])[:, None]
+    h[:, H // 3] = [2.0 ** 70, 2.0 ** 65, 2.0 ** 100, 2.0 ** 126, 2.0 ** 90, -2.0 ** 75]
+    w = g.standard_normal(H)
+    ht, wt = dev(h, torch.float32), dev(w, torch.float32)
+    h64, w64 = f64(ht), f64(wt)
+    want = h64 * ref.inverse_rms(h64, 1e-6) * w64
+    # r is off by 50 half steps, and there are three products; two of them may be subnormal
+    y, _ = moe.rms_norm(ht, wt)
+    assert_within(y, want, 55 * U32 * np.abs(want) + 2.0 ** -150 * (1 + np.abs(w64)), "y")
+    small = dev(np.full(H, 2.0 ** -120), torch.float32)
+    codes, scales, _ = moe.rms_norm_int8(ht, small)
+    codes64, s64 = ref.quantize(h64 * 2.0 ** -120)
+    want_s = s64 * ref.inverse_rms(h64, 1e-6)[:, 0]
+    assert np.array_equal(codes.cpu().numpy(), codes64)
+    assert_within(scales, want_s, 55 * U32 * want_s + 2.0 ** -150, "scales")
+    dy = dev(g.standard_normal((6, H)), torch.float32)
+    dx, dw = moe.rms_norm_grad(dy, ht, wt)
+    want, bound, want_w, bound_w = ref.norm_grad(f64(dy), h64, w64, 1e-6, None)
+    assert_within(dx, want, bound + U32 * np.abs(want) + 2.0 ** -148, "dx")
+    # (h / rms below 2^-126 is off by 2^-150, and so is each of six additions there)
+    assert_within(dw, want_w, bound_w + 2.0 ** -150 * (np.abs(f64(dy)).sum(axis=0) + 6), "dweight")
