@@ -66,41 +66,33 @@ struct AdaptArgs {
 
 constexpr int kStep = 64;  // depth of two matrix instructions
 
-// v of the tile's rows, NT * 16 ranks, over one part of the depth. WK of the block's four
-// waves share it among them, the others have rows of their own. P steps are on their way.
-template <typename T, int MS, int NT, int WK, int P>
+// v of the tile's 16 rows, NT * 16 ranks, over one part of the depth, which the block's four
+// waves share among them. P steps are on their way.
+template <typename T, int NT, int P>
 __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p) {
-    constexpr int WM = 4 / WK, BM = WM * MS * 16;
-    __shared__ f32x4 s_acc[WK > 1 ? WK : 1][WK > 1 ? MS * NT : 1][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WK, wk = wave % WK, c = lane & 15, q = lane >> 4;
+    __shared__ f32x4 s_acc[4][NT][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
     const int split = blockIdx.x % p.splits;
     int e, row0, rows;
-    if (!find_tile<BM>(p.offsets, p.n, p.T, blockIdx.x / p.splits, lane, &e, &row0, &rows)) return;
+    if (!find_tile<16>(p.offsets, p.n, p.T, blockIdx.x / p.splits, lane, &e, &row0, &rows)) return;
     const int r0 = blockIdx.y * NT * 16;
-    const T* xr[MS];
+    // (rows behind the last one and entries that name no token: any token, not used)
+    const int t = p.row_to_token[row0 + min(c, rows - 1)];
+    const T* xr = (const T*)p.x + (int64_t)((uint32_t)t < (uint32_t)p.T ? t : 0) * p.ld_x + 8 * q;
     const T* ar[NT];
-#pragma unroll
-    for (int m = 0; m < MS; ++m) {
-        // (rows behind the last one and entries that name no token: any token, not used)
-        const int row = row0 + min(wm * MS * 16 + m * 16 + c, rows - 1), t = p.row_to_token[row];
-        xr[m] = (const T*)p.x + (int64_t)((uint32_t)t < (uint32_t)p.T ? t : 0) * p.ld_x + 8 * q;
-    }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
         ar[j] = (const T*)p.a + e * p.a_adapter + (int64_t)min(r0 + j * 16 + c, p.r - 1) * p.ld_a + 8 * q;
-    f32x4 acc[MS][NT] = {};
+    f32x4 acc[NT] = {};
     const int steps = (p.H + kStep - 1) / kStep, each = (steps + p.splits - 1) / p.splits;
-    const int lo = split * each + wk, hi = min(steps, (split + 1) * each);
-    Vec<T> xv[P][MS][2], av[P][NT][2];
+    const int lo = split * each + wave, hi = min(steps, (split + 1) * each);
+    Vec<T> xv[P][2], av[P][NT][2];
     auto load = [&](int u, int s) INLINE {
         const int k = s * kStep;
         if (s >= hi) return;
         if (k + kStep <= p.H) {
 #pragma unroll
-            for (int m = 0; m < MS; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) xv[u][m][h] = load_vec(xr[m] + k + 32 * h);
+            for (int h = 0; h < 2; ++h) xv[u][h] = load_vec(xr + k + 32 * h);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -108,9 +100,7 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p) {
         } else {
             const bool in[2] = {k + 8 * q < p.H, k + 32 + 8 * q < p.H};  // (H is a multiple of 16)
 #pragma unroll
-            for (int m = 0; m < MS; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) xv[u][m][h] = in[h] ? load_vec(xr[m] + k + 32 * h) : Vec<T>{};
+            for (int h = 0; h < 2; ++h) xv[u][h] = in[h] ? load_vec(xr + k + 32 * h) : Vec<T>{};
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -118,52 +108,35 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs p) {
         }
     };
 #pragma unroll
-    for (int u = 0; u < P; ++u) load(u, lo + u * WK);
-    for (int s = lo; s < hi; s += P * WK) {
+    for (int u = 0; u < P; ++u) load(u, lo + u * 4);
+    for (int s = lo; s < hi; s += P * 4) {
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            if (s + u * WK >= hi) break;
+            if (s + u * 4 >= hi) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int m = 0; m < MS; ++m)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[m][j] = mma(av[u][j][h], xv[u][m][h], acc[m][j]);
-            load(u, s + (u + P) * WK);
+                for (int j = 0; j < NT; ++j) acc[j] = mma(av[u][j][h], xv[u][h], acc[j]);
+            load(u, s + (u + P) * 4);
         }
     }
-    // acc[m][j]: token m * 16 + c, ranks j * 16 + 4 q + 0..3
+    // acc[j]: token c, ranks j * 16 + 4 q + 0..3
+#pragma unroll
+    for (int j = 0; j < NT; ++j) s_acc[wave][j][lane] = acc[j];
+    __syncthreads();
     float* part = p.part + (int64_t)split * p.T * p.r;
-    auto put = [&](int m, int j, f32x4 v) INLINE {
-        const int row = wm * MS * 16 + m * 16 + c, rank = r0 + j * 16 + 4 * q;
-        if (row < rows && rank < p.r) *reinterpret_cast<f32x4*>(part + (int64_t)(row0 + row) * p.r + rank) = v;
-    };
-    if constexpr (WK == 1) {
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) put(m, j, acc[m][j]);
-    } else {
-        static_assert(WK == 4, "a tile's waves are the block's");
-#pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) s_acc[wk][m * NT + j][lane] = acc[m][j];
-        __syncthreads();
-#pragma unroll
-        for (int f = 0; f < MS * NT; ++f)
-            if (f % WK == wk) put(f / NT, f % NT, (s_acc[0][f][lane] + s_acc[1][f][lane]) + (s_acc[2][f][lane] + s_acc[3][f][lane]));
+    for (int j = 0; j < NT; ++j) {
+        const int rank = r0 + j * 16 + 4 * q;
+        if (j % 4 == wave && c < rows && rank < p.r)
+            *reinterpret_cast<f32x4*>(part + (int64_t)(row0 + c) * p.r + rank) =
+                (s_acc[0][j][lane] + s_acc[1][j][lane]) + (s_acc[2][j][lane] + s_acc[3][j][lane]);
     }
 }
 
-// out = base + scale b v: MS * 16 rows per block, 256 columns at a time (64 per wave), `chunks`
-// times, with the next columns' b and base on their way. A lane ends up with twice 8
-// consecutive columns of a row: the rows of b that it multiplies are dealt so.
-// KS: b's rows are at most 32 KS long and wait in registers (0: any length, read as
-// needed). Blocks behind the tiles copy the rows of tokens without an adapter.
 constexpr int kCopyTokens = 16;
 
-// The copy of one group of tokens.
+// The copy of one group of tokens without an adapter.
 template <typename T>
 __device__ __forceinline__ void copy_tokens(const AdaptArgs& p, int group) {
     const int tid = threadIdx.x, lane = tid & 63, t0 = group * kCopyTokens, t = t0 + (lane & 15);
@@ -194,9 +167,14 @@ __device__ __forceinline__ void split_value(float f, T* hi, T* mid, T* lo) {
     *lo = from_f32<T>(rest - to_f32(*mid));
 }
 
-template <typename T, int MS, int KS>
+// out = base + scale b v: 16 rows per block, 256 columns at a time (64 per wave), `chunks`
+// times, with the next columns' b and base on their way. A lane ends up with twice 8
+// consecutive columns of a row: the rows of b that it multiplies are dealt so.
+// KS: b's rows are at most 32 KS long and wait in registers (0: any length, read as
+// needed). Blocks behind the tiles copy the rows of tokens without an adapter.
+template <typename T, int KS>
 __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, int nblocks, int chunks) {
-    constexpr int BM = MS * 16, KR = KS ? KS : 1;
+    constexpr int BM = 16, KR = KS ? KS : 1;
     extern __shared__ __align__(16) char s_room[];
     __shared__ float s_back[BM];  // what undoes the tokens' powers of two, times the adapter's scale
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
@@ -207,23 +185,17 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
     }
     int e, row0, rows;
     if (!find_tile<BM>(p.offsets, p.n, p.T, tile, lane, &e, &row0, &rows)) return;
-    int64_t token[MS];
-#pragma unroll
-    for (int m = 0; m < MS; ++m) {
-        const int row = m * 16 + c, t = row < rows ? p.row_to_token[row0 + row] : -1;
-        token[m] = (uint32_t)t < (uint32_t)p.T ? t : -1;
-    }
+    const int t = c < rows ? p.row_to_token[row0 + c] : -1;
+    const int64_t token = (uint32_t)t < (uint32_t)p.T ? t : -1;
     const int first = (blockIdx.x % nblocks) * chunks * 256 + wave * 64;
     const T* b = (const T*)p.b + e * p.b_adapter;
-    Vec<T> base[MS][2], bv[KR][4];
+    Vec<T> base[2], bv[KR][4];
     auto load_base = [&](int n0) INLINE {
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int n = n0 + 32 * g + 8 * q;
-                if (token[m] >= 0 && n + 8 <= p.N) base[m][g] = load_vec((const T*)p.base + token[m] * p.ld_base + n);
-            }
+        for (int g = 0; g < 2; ++g) {
+            const int n = n0 + 32 * g + 8 * q;
+            if (token >= 0 && n + 8 <= p.N) base[g] = load_vec((const T*)p.base + token * p.ld_base + n);
+        }
     };
     auto load_b = [&](int n0, int k, Vec<T>* v) INLINE {
 #pragma unroll
@@ -273,8 +245,8 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
         for (int j = at * 4; j < deep; j += TPR * 4)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = row * wide + j + i;
-                split_value(ldexpf(v[at], up), &v_hi[at], &v_mid[at], &v_lo[at]);
+                const int o = row * wide + j + i;
+                split_value(ldexpf(v[o], up), &v_hi[o], &v_mid[o], &v_lo[o]);
             }
     }
     __syncthreads();
@@ -282,16 +254,13 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
         const int n0 = first + i * 256;
         if (n0 >= p.N) return;
         const bool more = i + 1 < chunks && n0 + 256 < p.N;
-        f32x4 acc[MS][4] = {};
+        f32x4 acc[4] = {};
         auto multiply = [&](int k, const Vec<T>* w) INLINE {
+            const Vec<T> hi = *reinterpret_cast<const Vec<T>*>(v_hi + c * wide + k);
+            const Vec<T> mid = *reinterpret_cast<const Vec<T>*>(v_mid + c * wide + k);
+            const Vec<T> lo = *reinterpret_cast<const Vec<T>*>(v_lo + c * wide + k);
 #pragma unroll
-            for (int m = 0; m < MS; ++m) {
-                const Vec<T> hi = *reinterpret_cast<const Vec<T>*>(v_hi + (m * 16 + c) * wide + k);
-                const Vec<T> mid = *reinterpret_cast<const Vec<T>*>(v_mid + (m * 16 + c) * wide + k);
-                const Vec<T> lo = *reinterpret_cast<const Vec<T>*>(v_lo + (m * 16 + c) * wide + k);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[m][u] = mma(w[u], hi, mma(w[u], mid, mma(w[u], lo, acc[m][u])));
-            }
+            for (int u = 0; u < 4; ++u) acc[u] = mma(w[u], hi, mma(w[u], mid, mma(w[u], lo, acc[u])));
         };
         if constexpr (KS > 0) {
 #pragma unroll
@@ -306,25 +275,23 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs p, int most, in
                 multiply(k, bv[0]);
             }
         }
-        // acc[m][u]: token m * 16 + c, columns n0 + 32 (u / 2) + 8 q + 4 (u % 2) + 0..3
-#pragma unroll
-        for (int m = 0; m < MS; ++m) {
-            if (token[m] < 0) continue;
-            const float back = s_back[m * 16 + c];
+        // acc[u]: token c, columns n0 + 32 (u / 2) + 8 q + 4 (u % 2) + 0..3
+        if (token >= 0) {
+            const float back = s_back[c];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const int n = n0 + 32 * g + 8 * q;
-                T* dst = (T*)p.out + token[m] * p.ld_out + n;
+                T* dst = (T*)p.out + token * p.ld_out + n;
                 if (n + 8 <= p.N) {
                     Vec<T> o;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o.e[j] = from_f32<T>(__fmaf_rn(acc[m][2 * g + j / 4][j % 4], back, to_f32(base[m][g].e[j])));
+                    for (int j = 0; j < 8; ++j) o.e[j] = from_f32<T>(__fmaf_rn(acc[2 * g + j / 4][j % 4], back, to_f32(base[g].e[j])));
                     store_vec<false>(dst, o);
                 } else {
-                    const T* src = (const T*)p.base + token[m] * p.ld_base + n;
+                    const T* src = (const T*)p.base + token * p.ld_base + n;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (n + j < p.N) dst[j] = from_f32<T>(__fmaf_rn(acc[m][2 * g + j / 4][j % 4], back, to_f32(src[j])));
+                        if (n + j < p.N) dst[j] = from_f32<T>(__fmaf_rn(acc[2 * g + j / 4][j % 4], back, to_f32(src[j])));
                 }
             }
         }
@@ -427,7 +394,7 @@ __global__ __launch_bounds__(256) void adapt_down_wide_kernel(AdaptArgs p, uint3
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into the LDS outlives the block
 }
 
-// out = base + scale b v for 4 * MS * 16 rows, 128 columns at a time, `chunks` times. The block's
+// out = base + scale b v for 64 rows, 16 a wave, 128 columns at a time, `chunks` times. The block's
 // waves share the columns' rows of b in the LDS (two buffers) and have rows of their own,
 // whose v waits in registers. Lane (c, q) holds columns 8 c .. 8 c + 7 of tokens 4 q .. 4 q + 3:
 // row 8 c + u of b is column c of instruction u and lies in row 16 u + c of the buffer, its
@@ -436,9 +403,9 @@ __global__ __launch_bounds__(256) void adapt_down_wide_kernel(AdaptArgs p, uint3
 // Ranks of 65 to 128 take 264 registers, of which 256 let two waves of a SIMD run: held to
 // them (six are spilled) the call of 16384 tokens, H = 7168, N = 4096, rank 128, takes 228 us
 // instead of 268.
-template <typename T, int MS, int KS>
+template <typename T, int KS>
 __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(AdaptArgs p, int most, int nblocks, int chunks) {
-    constexpr int BM = 64 * MS, kColumns = 128;
+    constexpr int BM = 64, kColumns = 128;
     extern __shared__ __align__(1024) char s_room[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
     const int tile = blockIdx.x / nblocks;
@@ -467,13 +434,12 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
     const uint32_t room = lds_address(s_room);
     issue(first, 0);
     // v of the wave's rows (those behind the last are the last one's again)
-    Vec<T> hi[MS][KS], mid[MS][KS], lo[MS][KS];
-    float back[MS][4];
-    int token[MS][4];
-#pragma unroll
-    for (int m = 0; m < MS; ++m) {
-        const int row = row0 + min((wave * MS + m) * 16 + c, rows - 1);
-        const int t = p.row_to_token[row], named = (uint32_t)t < (uint32_t)p.T && (wave * MS + m) * 16 + c < rows ? t : -1;
+    Vec<T> hi[KS], mid[KS], lo[KS];
+    float back[4];
+    int token[4];
+    {
+        const int row = wave * 16 + c, t = p.row_to_token[row0 + min(row, rows - 1)];
+        const int named = (uint32_t)t < (uint32_t)p.T && row < rows ? t : -1;
         float f[KS][8];
         uint32_t top = 0;
 #pragma unroll
@@ -482,7 +448,7 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[s][i] = 0.0f;
             if (k < p.r) {
-                const float* src = p.part + (int64_t)row * p.r + k;
+                const float* src = p.part + (int64_t)(row0 + min(row, rows - 1)) * p.r + k;
                 for (int z = 0; z < p.splits; ++z, src += (int64_t)p.T * p.r) {
                     const f32x4 u = *reinterpret_cast<const f32x4*>(src), w = *reinterpret_cast<const f32x4*>(src + 4);
 #pragma unroll
@@ -501,37 +467,31 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
         const float undo = ldexpf(p.scales ? p.scales[e] : 1.0f, -up);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            back[m][i] = __shfl(undo, 4 * q + i);
-            token[m][i] = __shfl(named, 4 * q + i);
+            back[i] = __shfl(undo, 4 * q + i);
+            token[i] = __shfl(named, 4 * q + i);
         }
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) split_value(ldexpf(f[s][i], up), &hi[m][s].e[i], &mid[m][s].e[i], &lo[m][s].e[i]);
+            for (int i = 0; i < 8; ++i) split_value(ldexpf(f[s][i], up), &hi[s].e[i], &mid[s].e[i], &lo[s].e[i]);
     }
-    // Base of a pass, always MS * 4 loads (none where a row has no 8 columns: then there is one
+    // Base of a pass, always four loads (none where a row has no 8 columns: then there is one
     // pass), so that the wait below can count them.
-    typedef u32x4 Base[MS][4];
+    typedef u32x4 Base[4];
     auto load_base = [&](int n0, Base& base) INLINE {
         if (p.N < 8) return;
         const int n = min(n0 + 8 * c, p.N - 8);
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) base[m][i] = __builtin_bit_cast(u32x4, load_vec((const T*)p.base + max(token[m][i], 0) * p.ld_base + n));
+        for (int i = 0; i < 4; ++i) base[i] = __builtin_bit_cast(u32x4, load_vec((const T*)p.base + max(token[i], 0) * p.ld_base + n));
     };
     // Makes the compiler wait for these loads here, and not where the values are used.
     auto have = [](Base& base) INLINE {
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(base[m][i]));
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(base[i]));
     };
     bool named = true;  // all rows of the wave
 #pragma unroll
-    for (int m = 0; m < MS; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) named &= token[m][i] >= 0;
+    for (int i = 0; i < 4; ++i) named &= token[i] >= 0;
     named = __ballot(!named) == 0;
     const int end = min(first + chunks * kColumns, p.N);
     auto pass = [&](int n0, int buf, Base& base, Base& next) INLINE {
@@ -541,7 +501,7 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
             asm volatile("" ::: "memory");  // (the count below wants them in this order)
             load_base(n0 + kColumns, next);
         }
-        f32x4 acc[MS][8] = {};
+        f32x4 acc[8] = {};
         const uint32_t rows_of_b = room + buf * size + c * pitch;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -555,40 +515,35 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
             for (int u = 0; u < 8; ++u) {
                 if (p.r % 32 && k >= rc) v[u] = u32x4{};
                 const Vec<T> bv = __builtin_bit_cast(Vec<T>, v[u]);
-#pragma unroll
-                for (int m = 0; m < MS; ++m) acc[m][u] = mma(hi[m][s], bv, mma(mid[m][s], bv, mma(lo[m][s], bv, acc[m][u])));
+                acc[u] = mma(hi[s], bv, mma(mid[s], bv, mma(lo[s], bv, acc[u])));
             }
         }
         const int n = n0 + 8 * c;
-        auto result = [&](int m, int i) INLINE {
-            const Vec<T> old = __builtin_bit_cast(Vec<T>, base[m][i]);
+        auto result = [&](int i) INLINE {
+            const Vec<T> old = __builtin_bit_cast(Vec<T>, base[i]);
             Vec<T> o;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) o.e[u] = from_f32<T>(__fmaf_rn(acc[m][u][i], back[m][i], to_f32(old.e[u])));
+            for (int u = 0; u < 8; ++u) o.e[u] = from_f32<T>(__fmaf_rn(acc[u][i], back[i], to_f32(old.e[u])));
             return o;
         };
         if (named && n0 + kColumns <= p.N) {
 #pragma unroll
-            for (int m = 0; m < MS; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) store_vec<false>((T*)p.out + token[m][i] * p.ld_out + n, result(m, i));
+            for (int i = 0; i < 4; ++i) store_vec<false>((T*)p.out + token[i] * p.ld_out + n, result(i));
             return;
         }
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
+        for (int i = 0; i < 4; ++i) {
+            if (token[i] < 0) continue;
+            T* dst = (T*)p.out + token[i] * p.ld_out + n;
+            if (n + 8 <= p.N) {
+                store_vec<false>(dst, result(i));
+            } else {
+                const T* src = (const T*)p.base + token[i] * p.ld_base + n;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (token[m][i] < 0) continue;
-                T* dst = (T*)p.out + token[m][i] * p.ld_out + n;
-                if (n + 8 <= p.N) {
-                    store_vec<false>(dst, result(m, i));
-                } else {
-                    const T* src = (const T*)p.base + token[m][i] * p.ld_base + n;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (n + u < p.N) dst[u] = from_f32<T>(__fmaf_rn(acc[m][u][i], back[m][i], to_f32(src[u])));
-                }
+                for (int u = 0; u < 8; ++u)
+                    if (n + u < p.N) dst[u] = from_f32<T>(__fmaf_rn(acc[u][i], back[i], to_f32(src[u])));
             }
+        }
         have(next);
     };
     Base one, two;
@@ -597,11 +552,11 @@ __global__ __launch_bounds__(256, KS == 4 ? 2 : 1) void adapt_up_wide_kernel(Ada
     for (int n0 = first; n0 < end; n0 += 2 * kColumns) {
         pass(n0, 0, one, two);
         if (n0 + kColumns >= end) break;
-        // the next columns' rows of b have landed once no more than MS * 4 operations are left: behind
+        // the next columns' rows of b have landed once no more than four operations are left: behind
         // them came as many loads of base, and whatever stores
-        wait_and_barrier<MS * 4>();
+        wait_and_barrier<4>();
         pass(n0 + kColumns, 1, two, one);
-        if (n0 + 2 * kColumns < end) wait_and_barrier<MS * 4>();
+        if (n0 + 2 * kColumns < end) wait_and_barrier<4>();
     }
 }
 
@@ -648,9 +603,9 @@ static void launch_down(const AdaptArgs& p, bool wide, hipStream_t s) {
 #undef MORE
     } else {
 #define MORE p
-        if (p.r <= 16) D((adapt_down_kernel<T, 1, 1, 4, 3>), 1);
-        else if (p.r <= 32) D((adapt_down_kernel<T, 1, 2, 4, 3>), 2);
-        else D((adapt_down_kernel<T, 1, 4, 4, 3>), 4);
+        if (p.r <= 16) D((adapt_down_kernel<T, 1, 3>), 1);
+        else if (p.r <= 32) D((adapt_down_kernel<T, 2, 3>), 2);
+        else D((adapt_down_kernel<T, 4, 3>), 4);
 #undef MORE
     }
 #undef D
@@ -668,14 +623,14 @@ static hipError_t launch_up(const AdaptArgs& p, bool wide, hipStream_t s) {
 #define U(KERNEL)                                                                                                      \
     hipLaunchKernelGGL((KERNEL), dim3((int)most * nblocks + copy), dim3(256), lds, s, p, (int)most, nblocks, chunks)
     if (wide) {
-        if (p.r <= 32) U((adapt_up_wide_kernel<T, 1, 1>));
-        else if (p.r <= 64) U((adapt_up_wide_kernel<T, 1, 2>));
-        else if (p.r <= 128) U((adapt_up_wide_kernel<T, 1, 4>));
-        else U((adapt_up_wide_kernel<T, 1, 8>));
+        if (p.r <= 32) U((adapt_up_wide_kernel<T, 1>));
+        else if (p.r <= 64) U((adapt_up_wide_kernel<T, 2>));
+        else if (p.r <= 128) U((adapt_up_wide_kernel<T, 4>));
+        else U((adapt_up_wide_kernel<T, 8>));
     } else {
-        if (p.r <= 32) U((adapt_up_kernel<T, 1, 1>));
-        else if (p.r <= 64) U((adapt_up_kernel<T, 1, 2>));
-        else U((adapt_up_kernel<T, 1, 0>));
+        if (p.r <= 32) U((adapt_up_kernel<T, 1>));
+        else if (p.r <= 64) U((adapt_up_kernel<T, 2>));
+        else U((adapt_up_kernel<T, 0>));
     }
 #undef U
     return hipGetLastError();
