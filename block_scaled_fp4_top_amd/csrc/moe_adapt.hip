@@ -18,9 +18,9 @@
 // adapter, where nothing but latency counts. The wide ones go through the LDS, filled by
 // direct loads of whole lines, and end with whole lines of base and out.
 //
-// 16384 tokens of 16 adapters of rank 64, H = 7168, N = 4096, bf16 (503 MB, 103 us of memory): 68
-// and 67 us (3.7 and 4.1 TB/s), straight from memory 108 and 126. 64 tokens of 32 adapters of
-// rank 16: 4.6 and 5.5 us; one token 3.5 and 4.7. (One launch for few tokens, whose blocks each
+// 16384 tokens of 16 adapters of rank 64, H = 7168, N = 4096, bf16 (503 MB, 103 us of memory): 69
+// us each (3.6 and 4.0 TB/s), straight from memory 108 and 126. 64 tokens of 32 adapters of
+// rank 16: 4.3 and 5.3 us; one token 3.5 and 4.7. (One launch for few tokens, whose blocks each
 // make all of v, takes 13 us: the address units again.)
 #include <algorithm>
 
@@ -577,6 +577,9 @@ struct AdaptPlan {
 // The wide kernels from 2048 tokens and 32 an adapter on. H = 7168, N = 4096, in a graph, us, wide
 // (narrow): rank 16, 1024 tokens of one adapter 17.8 (14.9), 2048 of 64 28.2 (30.2), 4096 of 64
 // 35 (56), of 128 43 (51), of 256 78 (53); rank 64 31 (25), 60 (62), 70 (114), 100 (118), 144 (134).
+// All n adapters have tokens there, which is what the rule takes for granted (the host does not
+// know how many do): 16384 tokens of 4 adapters take 148 us of rank 64 out of 4 or 166 out of
+// 512, but 275 out of 1024, by the narrow kernels.
 static AdaptPlan plan_adapt(int T, int n, int H) {
     AdaptPlan q;
     q.wide = T >= 2048 && T >= 32 * (int64_t)std::min(n, T);

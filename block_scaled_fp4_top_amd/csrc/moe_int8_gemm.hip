@@ -103,10 +103,12 @@ struct __attribute__((packed, aligned(sizeof(T)))) Few {
     T e[N];
 };
 
-// buffer_load_lds16's ONCE is for the rows of B of an expert with one M-tile. 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us then;
+// Rows of B of an expert with one M-tile are read once, past the caches
+// (buffer_load_lds16's ONCE): 64 x 8 routes over 256 experts of 4096 x 7168 801 -> 714 us;
 // mean rows of 16, 48, 64, 128 over 128 experts of 4096 x 4096 359 -> 325, 406 -> 377,
 // 422 -> 404, 516 -> 504 (with all of B non-temporal 326, 391, 443, 540: experts with
 // several tiles then lose their L2).
+
 // Stores N consecutive results of one row past the caches (nothing reads them here
 // again; with normal stores they push rows of A and B out of the L2: 16384 x 4096 x
 // 7168 went from 454 to 437 us, 98304 x 2048 x 2048 in 64 groups from 525 to 482).

@@ -195,8 +195,8 @@ __global__ __launch_bounds__(TPT < 256 ? 256 : TPT) void rms_norm_kernel(NormArg
 // With n = h r and g = dy w:  dx = r (g - n mean(g n)) (+ dtotal),  dw = sum over rows of dy n.
 // dw: every block sums its rows in registers, in order, and leaves one row of partial
 // sums in the workspace, which a second kernel adds in the order of the blocks.
-// Bound by memory: 4096 x 4096 bf16 with dtotal (134 MB and 17 MB of partial sums) 26.8 and
-// 4.3 us from memory, 16384 x 7168 without (705 MB) 140 us. In a graph 25 and 141 us with 512 blocks, 29 and 161 with
+// Bound by memory: 4096 x 4096 bf16 with dtotal (134 MB and 17 MB of partial sums) 25 - 27 and
+// 4.2 us from memory, 16384 x 7168 without (705 MB) 140 us. In a graph 25 and 141 us with 512 blocks, 29 and 161 with
 // 256 (too little on its way), 25 and 156 with 1024 (partial sums).
 template <typename T, typename W>
 struct NormGradArgs {

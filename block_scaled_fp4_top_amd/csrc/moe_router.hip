@@ -20,11 +20,16 @@
 // values.
 //
 // Bound by the vector units: 16383 tokens, 256 experts, K = 8, fp32 (16.8 MB, 3.4 us of
-// memory) 12 us by sigmoid and bias, 13.5 - 18 with 8 groups too (1214 vector instructions
-// for four tokens: 374 the rounds, 186 the groups), 8 us by bf16 logits alone. With fp64 scores
-// and 64-bit rounds throughout 28 us. A launch ends with its slowest wave, so what a few tokens
-// need is kept short: a fallback of a whole wave of tokens to fp64 cost 8 us at the end (and
-// what is left of it is the range above).
+// memory) 13 us by sigmoid and bias, 13.5 - 18 with 8 groups too (1235 vector instructions
+// for four tokens, counted), 8 us by bf16 logits alone. With fp64 scores and 64-bit rounds
+// throughout 28 us. A launch ends with its slowest wave, so what a few tokens need is kept
+// short: a fallback of a whole wave of tokens to fp64 cost 8 us at the end (and what is left
+// of it is the range above).
+//
+// Two kinds of tokens always need the exact choice, one after the other in their wave: those
+// with equal groups at the border (padded rows of zeros with equal biases and sums of two:
+// half of 16383 tokens such rows, 87 us), and those of whose experts one lies further above
+// the rest than the keys reach (a bias of 3 for one expert, 90 us; with groups 100).
 #include <algorithm>
 
 #include "moe_args.h"

@@ -367,7 +367,7 @@ int moe_rms_norm_grad(const void* dy, int64_t dy_stride, const void* h, int64_t 
 
 /* The activation between an expert's two products, on sorted rows (moe_act):
  *   swiglu: a_j = silu(h_j) h_{I+j}, h: [rows][2I];  relu2: a_j = max(h_j, 0)^2, h: [rows][I]
- *   out[m][j] = w a_j, rounded once to dtype, with w = weights[row_to_route[m]] (the
+ *   out[m][j] = w a_j, in fp32 and rounded once to dtype, with w = weights[row_to_route[m]] (the
  *   router's weight on the input side of the second product), 1 where weights is NULL.
  *   offsets ([E+1]): only the rows below offsets[E] are read and written; NULL: all rows.
  *   weights ([rows], i.e. [T][K]) need offsets and row_to_route; rows whose entry names
